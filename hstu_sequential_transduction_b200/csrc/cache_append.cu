@@ -1,0 +1,222 @@
+// Append to the 8-bit key/value cache: quantise a call's history tokens into
+// their sequences' pages.
+//
+// Per block (page, head) of 64 tokens: amax over the block's new tokens, scale
+// 2^e with amax <= 448 2^e, code = E4M3(x 2^-e); a partly filled block keeps the
+// larger of its old scale and the new one, and its older codes are shifted to it.
+//
+// Bound by HBM: each k and v element is read once and its code written once.
+// One CTA per (sequence, block, head), 2 D threads: a thread takes 4 tokens x 8
+// dims of K and of V, all eight 16-byte (bf16) loads in flight before the one
+// reduction.  Keys leave as 8 bytes per token (16 lanes fill a 128-byte row).
+// Values are stored transposed: a thread packs its 4 tokens of each dim into a
+// word, the words cross through shared memory (columns XORed with the dim group
+// and odd groups one dim out of step, so the 32 words of a store fall into 32
+// banks) and leave as 16-byte pieces of 64-byte rows.
+#include <algorithm>
+
+#include "cache.cuh"
+
+namespace hstu {
+
+namespace {
+
+// eight elements to floats
+__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float *v)
+{
+    const uint4 w = *reinterpret_cast<const uint4 *>(p);
+    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+        v[2 * e] = __uint_as_float(ww[e] << 16);
+        v[2 * e + 1] = __uint_as_float(ww[e] & 0xffff0000u);
+    }
+}
+
+__device__ __forceinline__ void load8(const float *p, float *v)
+{
+    const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+
+// four codes re-rounded after a change of scale (ratio = old scale / new scale)
+__device__ __forceinline__ uint32_t rescale4(uint32_t codes, float ratio)
+{
+    const float2 lo = e4m3x2_to_f32x2(codes), hi = e4m3x2_to_f32x2(codes >> 16);
+    return f32x2_to_e4m3x2(lo.x * ratio, lo.y * ratio) | (f32x2_to_e4m3x2(hi.x * ratio, hi.y * ratio) << 16);
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(2 * D)
+cache_append_kernel(const CacheCall c, const T *__restrict__ k, int64_t ldk, const T *__restrict__ v, int64_t ldv,
+                    int32_t *__restrict__ new_lens, int32_t *__restrict__ new_pos, int blocks)
+{
+    __shared__ uint32_t sv[D * 16];
+    __shared__ uint32_t smax[2][D / 16];
+    const int h = (int)(blockIdx.x % (unsigned)c.H);
+    const int j = (int)(blockIdx.x / (unsigned)c.H % (unsigned)blocks);
+    const int b = (int)(blockIdx.x / ((unsigned)c.H * (unsigned)blocks));
+    CacheSeq s = cache_seq(c, b);
+    if (!s.bits && (int64_t)s.len + s.hist > (int64_t)c.max_pages * kPage)
+        s.bits = FLAG_CACHE_LEN;
+    const int count = s.bits ? 0 : s.hist;
+    if (j == 0 && h == 0 && threadIdx.x == 0) {
+        new_lens[b] = c.cache_lens[b] + count;
+        if (new_pos)
+            new_pos[b] = s.pos + count;
+        int bits = s.bits;
+        if (b == 0 && c.seq_offsets[0] != 0)
+            bits |= FLAG_OFFSET0;
+        if (b == c.B - 1 && c.seq_offsets[c.B] != c.T)
+            bits |= FLAG_TOTAL;
+        if (bits)
+            atomicOr(&c.hdr->flag, bits);
+    }
+    const int blk = s.len / kPage + j;                   // block of the sequence
+    const int a = j == 0 ? s.len - blk * kPage : 0;      // first new slot of the block
+    const int end = min(s.len + count - blk * kPage, kPage);
+    if (a >= end)
+        return;
+    const int page = table_page(c.table, c, b, blk);
+    if (page < 0) {
+        if (h == 0 && threadIdx.x == 0)
+            atomicOr(&c.hdr->flag, FLAG_CACHE_PAGE);
+        return;
+    }
+    const int part = threadIdx.x % (D / 8), quad = threadIdx.x / (D / 8);
+    const int t0 = 4 * quad;
+    // row of slot t: the sequence's token blk * 64 + t - len
+    const int64_t row0 = s.s0 + (int64_t)blk * kPage - s.len;
+
+    float x[4][8], y[4][8];
+    uint32_t mk = 0, mv = 0;
+#pragma unroll
+    for (int t = 0; t < 4; t++) {
+        const bool fresh = t0 + t >= a && t0 + t < end;
+        if (fresh) {
+            load8(k + (row0 + t0 + t) * ldk + (int64_t)h * D + 8 * part, x[t]);
+            load8(v + (row0 + t0 + t) * ldv + (int64_t)h * D + 8 * part, y[t]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; e++)
+                x[t][e] = y[t][e] = 0.f;
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < 4; t++)
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+            mk = max(mk, __float_as_uint(x[t][e]) & 0x7fffffffu);
+            mv = max(mv, __float_as_uint(y[t][e]) & 0x7fffffffu);
+        }
+    mk = __reduce_max_sync(0xffffffffu, mk);
+    mv = __reduce_max_sync(0xffffffffu, mv);
+    if ((threadIdx.x & 31) == 0) {
+        smax[0][threadIdx.x >> 5] = mk;
+        smax[1][threadIdx.x >> 5] = mv;
+    }
+    const int64_t si = (int64_t)page * c.H + h;
+    const float kold = a > 0 ? c.k_scale[si] : 0.f, vold = a > 0 ? c.v_scale[si] : 0.f;
+    __syncthreads();
+    mk = mv = 0;
+#pragma unroll
+    for (int w = 0; w < D / 16; w++) {
+        mk = max(mk, smax[0][w]);
+        mv = max(mv, smax[1][w]);
+    }
+    const float ks = larger_scale(block_scale(mk), kold), vs = larger_scale(block_scale(mv), vold);
+    const float ki = scale_inverse(ks), vi = scale_inverse(vs);
+    if (threadIdx.x == 0) {  // after the barrier: every thread has read the old scales
+        c.k_scale[si] = ks;
+        c.v_scale[si] = vs;
+    }
+    uint8_t *kc = c.k_codes + block_offset<D>(page, c.H, h);
+    uint8_t *vc = c.v_codes + block_offset<D>(page, c.H, h);
+    const float kratio = kold * ki, vratio = vold * vi;
+#pragma unroll
+    for (int t = 0; t < 4; t++) {
+        uint2 *dst = reinterpret_cast<uint2 *>(kc + (t0 + t) * D + 8 * part);
+        if (t0 + t >= a && t0 + t < end) {
+            uint2 w;
+            w.x = f32x2_to_e4m3x2(x[t][0] * ki, x[t][1] * ki) | (f32x2_to_e4m3x2(x[t][2] * ki, x[t][3] * ki) << 16);
+            w.y = f32x2_to_e4m3x2(x[t][4] * ki, x[t][5] * ki) | (f32x2_to_e4m3x2(x[t][6] * ki, x[t][7] * ki) << 16);
+            *dst = w;
+        } else if (t0 + t < a && kratio != 1.f) {
+            const uint2 w = *dst;
+            *dst = make_uint2(rescale4(w.x, kratio), rescale4(w.y, kratio));
+        }
+    }
+#pragma unroll
+    for (int ee = 0; ee < 8; ee++) {
+        const int e = ee ^ (part & 1), d = 8 * part + e;
+        // select y[.][e] without a dynamic index
+        float y4[4];
+#pragma unroll
+        for (int t = 0; t < 4; t++)
+            y4[t] = (part & 1) ? y[t][ee ^ 1] : y[t][ee];
+        uint32_t w = f32x2_to_e4m3x2(y4[0] * vi, y4[1] * vi) | (f32x2_to_e4m3x2(y4[2] * vi, y4[3] * vi) << 16);
+        if (t0 < a || t0 + 4 > end) {  // some of these slots are not new: shifted if older, kept if behind the end
+            const uint32_t was = *reinterpret_cast<const uint32_t *>(vc + d * kPage + t0);
+            const uint32_t moved = vratio != 1.f ? rescale4(was, vratio) : was;
+            uint32_t mix = 0;
+#pragma unroll
+            for (int t = 0; t < 4; t++) {
+                const uint32_t m = 0xffu << (8 * t);
+                mix |= m & (t0 + t < a ? moved : (t0 + t < end ? w : was));
+            }
+            w = mix;
+        }
+        sv[d * 16 + (quad ^ (part & 15))] = w;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < D * 4; i += 2 * D) {
+        const int d = i >> 2, q = (i & 3) * 4, z = (d >> 3) & 15;
+        *reinterpret_cast<uint4 *>(vc + d * kPage + 4 * q) =
+            make_uint4(sv[d * 16 + (q ^ z)], sv[d * 16 + ((q + 1) ^ z)], sv[d * 16 + ((q + 2) ^ z)],
+                       sv[d * 16 + ((q + 3) ^ z)]);
+    }
+    if (h == 0) {
+        for (int t = threadIdx.x; t < kPage; t += 2 * D) {
+            if (t < a || t >= end)
+                continue;
+            const int64_t at = (int64_t)page * kPage + t;
+            const int i = blk * kPage + t - s.len;
+            c.timestamps[at] = c.ts[s.s0 + i];
+            c.positions[at] = s.pos + i;
+            if (c.weights)
+                c.weights[at] = 0.f;
+        }
+    }
+}
+
+template <typename T, int D>
+cudaError_t append(const CacheCall &c, const void *k, int64_t ldk, const void *v, int64_t ldv, int32_t *new_lens,
+                   int32_t *new_pos, int blocks, cudaStream_t stream)
+{
+    const int64_t grid = (int64_t)c.B * blocks * c.H;
+    cache_append_kernel<T, D><<<(unsigned)grid, 2 * D, 0, stream>>>(c, static_cast<const T *>(k), ldk,
+                                                                    static_cast<const T *>(v), ldv, new_lens, new_pos,
+                                                                    blocks);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+// blocks a sequence's new tokens may touch: they start anywhere in the first
+int cache_append_blocks(int max_seq_len) { return std::max(1, (int)(((int64_t)max_seq_len + 2 * kPage - 2) / kPage)); }
+
+cudaError_t launch_cache_append(const CacheCall &c, bool bf16, const void *k, int64_t ldk, const void *v, int64_t ldv,
+                                int32_t *new_lens, int32_t *new_pos, cudaStream_t stream)
+{
+    if (c.B == 0)
+        return cudaSuccess;
+    const int blocks = cache_append_blocks(c.max_seq_len);
+    if (bf16)
+        return c.d == 64 ? append<__nv_bfloat16, 64>(c, k, ldk, v, ldv, new_lens, new_pos, blocks, stream)
+                         : append<__nv_bfloat16, 128>(c, k, ldk, v, ldv, new_lens, new_pos, blocks, stream);
+    return c.d == 32 ? append<float, 32>(c, k, ldk, v, ldv, new_lens, new_pos, blocks, stream)
+                     : append<float, 64>(c, k, ldk, v, ldv, new_lens, new_pos, blocks, stream);
+}
+
+}  // namespace hstu

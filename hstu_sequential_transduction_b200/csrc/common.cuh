@@ -33,6 +33,8 @@ enum : int {
 
 // A pipeline wait that runs out records FLAG_TIMEOUT in the header's flag.
 enum : int { FLAG_TIMEOUT = 32 };
+// 8-bit cache: a length outside its bounds, a page outside the pool.
+enum : int { FLAG_CACHE_LEN = 64, FLAG_CACHE_PAGE = 128 };
 constexpr long long kWaitLimitCycles = 4000000000LL;  // ~2 s at 2 GHz
 // the limit under the bounded-wait test hook (HSTU_DEBUG_WAIT_TEST): ~1 ms, far
 // above any wait of a working pipeline (a few tile times), short for a test

@@ -1,5 +1,6 @@
 // C ABI of libhstu: argument validation, workspace carving and kernel dispatch.
 // Every check that can fail runs on the host before anything is enqueued.
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <cstring>
@@ -228,6 +229,73 @@ hstu_status attn_bwd_strided(const hstu_attn_desc *desc, const void *q, int64_t 
     HSTU_TRY(schedule(desc, seq_offsets, num_targets, 0, workspace, st));
     return cuda_status(launch_attn_bwd_f32(p, grid_items(desc), st));
 }
+
+// ---- 8-bit cache ---------------------------------------------------------------
+
+hstu_status check_cache(const hstu_cache *c)
+{
+    if (!c || c->num_pages < 0 || c->num_heads < 1 || c->max_pages < 0)
+        return HSTU_ERR_INVALID_ARG;
+    if (c->head_dim != 32 && c->head_dim != 64 && c->head_dim != 128)
+        return HSTU_ERR_UNSUPPORTED;
+    if ((int64_t)c->max_pages * HSTU_CACHE_PAGE > INT_MAX)
+        return HSTU_ERR_UNSUPPORTED;
+    if (c->num_pages > 0 && (!c->k_codes || !c->v_codes || !c->k_scale || !c->v_scale || !c->timestamps ||
+                             !c->positions || !aligned16(c->k_codes) || !aligned16(c->v_codes)))
+        return HSTU_ERR_INVALID_ARG;
+    return HSTU_OK;
+}
+
+CacheCall cache_call(const hstu_cache *c, int32_t B, int32_t max_cache_len, const int32_t *table,
+                     const int32_t *lens, void *ws)
+{
+    CacheCall p{};
+    p.k_codes = c->k_codes;
+    p.v_codes = c->v_codes;
+    p.k_scale = c->k_scale;
+    p.v_scale = c->v_scale;
+    p.timestamps = c->timestamps;
+    p.positions = c->positions;
+    p.weights = c->weights;
+    p.num_pages = c->num_pages;
+    p.H = c->num_heads;
+    p.d = c->head_dim;
+    p.max_pages = c->max_pages;
+    p.B = B;
+    p.max_cache_len = max_cache_len;
+    p.table = table;
+    p.cache_lens = lens;
+    p.hdr = static_cast<WsHeader *>(ws);
+    return p;
+}
+
+// rows `stride` elements apart of a [T, H, d] tensor: dense enough and 16-byte aligned
+bool row_stride_ok(int64_t stride, int64_t width, size_t elem) { return stride >= width && stride * elem % 16 == 0; }
+
+hstu_status check_cache_attn(const hstu_attn_desc *d, const hstu_cache *c, int32_t max_cache_len)
+{
+    HSTU_TRY(check_attn_desc(d));
+    HSTU_TRY(check_cache(c));
+    if (max_cache_len < 0 || d->num_heads != c->num_heads || d->d_qk != c->head_dim)
+        return HSTU_ERR_INVALID_ARG;
+    if (d->fp8_qk || d->debug_checks || d->local_window || d->global_window)
+        return HSTU_ERR_UNSUPPORTED;
+    // a longer cache than the tables have room for is never read
+    if (max_cache_len > c->max_pages * HSTU_CACHE_PAGE)
+        return HSTU_ERR_INVALID_ARG;
+    return HSTU_OK;
+}
+
+CacheCall cache_attn_call(const hstu_attn_desc *d, const hstu_cache *c, int32_t max_cache_len)
+{
+    CacheCall p = cache_call(c, d->num_seqs, max_cache_len, nullptr, nullptr, nullptr);
+    p.T = d->total_tokens;
+    p.max_seq_len = (int)std::min<int64_t>(d->max_seq_len, d->total_tokens);
+    return p;
+}
+
+// blocks of a launch that must stay below the grid limit
+bool grid_ok(int64_t a, int64_t b, int64_t c) { return (double)a * (double)b * (double)c < 2147483647.0; }
 
 }  // namespace
 
@@ -711,6 +779,160 @@ hstu_status hstu_gemm_e4m3(const void *codes, const float *scales, int64_t M, in
     HSTU_CUDA(cudaMemsetAsync(workspace, 0, sizeof(WsHeader), st));
     return cuda_status(launch_gemm_e4m3(codes, K, scales, wpack, K, ws, bias, y, N, M, N, K, apply_silu != 0,
                                         static_cast<WsHeader *>(workspace), st));
+}
+
+hstu_status hstu_cache_append_workspace_size(size_t *bytes)
+{
+    if (!bytes)
+        return HSTU_ERR_INVALID_ARG;
+    *bytes = sizeof(WsHeader);
+    return HSTU_OK;
+}
+
+hstu_status hstu_cache_append(const hstu_cache *cache, int32_t dtype, int32_t num_seqs, int32_t max_seq_len,
+                              int64_t total_tokens, const void *k, int64_t k_stride, const void *v,
+                              int64_t v_stride, const int64_t *seq_offsets, const int64_t *timestamps,
+                              const int32_t *num_targets, const int32_t *block_table, const int32_t *cache_lens,
+                              const int32_t *seq_pos, int32_t *new_lens, int32_t *new_pos, void *workspace,
+                              size_t workspace_bytes, void *stream)
+{
+    HSTU_TRY(check_cache(cache));
+    if (dtype != HSTU_F32 && dtype != HSTU_BF16)
+        return HSTU_ERR_INVALID_ARG;
+    const bool bf16 = dtype == HSTU_BF16;
+    const int d = cache->head_dim;
+    if (bf16 ? d != 64 && d != 128 : d != 32 && d != 64)
+        return HSTU_ERR_UNSUPPORTED;
+    if (num_seqs < 0 || max_seq_len < 0 || total_tokens < 0 || !seq_offsets)
+        return HSTU_ERR_INVALID_ARG;
+    if (num_seqs > 0 && (!cache_lens || !new_lens || (cache->max_pages > 0 && !block_table)))
+        return HSTU_ERR_INVALID_ARG;
+    if (new_lens && (new_lens == cache_lens || new_lens == seq_pos || new_lens == new_pos))
+        return HSTU_ERR_INVALID_ARG;
+    if (new_pos && (new_pos == cache_lens || new_pos == seq_pos))
+        return HSTU_ERR_INVALID_ARG;
+    const int64_t width = (int64_t)cache->num_heads * d;
+    const size_t elem = bf16 ? 2 : 4;
+    if (total_tokens > 0 && (!k || !v || !timestamps || !aligned16(k) || !aligned16(v) ||
+                             !row_stride_ok(k_stride, width, elem) || !row_stride_ok(v_stride, width, elem)))
+        return HSTU_ERR_INVALID_ARG;
+    HSTU_TRY(check_ws(workspace, workspace_bytes, sizeof(WsHeader)));
+    CacheCall c = cache_call(cache, num_seqs, INT_MAX, block_table, cache_lens, workspace);
+    c.T = total_tokens;
+    c.max_seq_len = (int)std::min<int64_t>(max_seq_len, total_tokens);
+    c.seq_offsets = seq_offsets;
+    c.num_targets = num_targets;
+    c.ts = timestamps;
+    c.seq_pos = seq_pos;
+    if (!grid_ok(num_seqs, cache_append_blocks(c.max_seq_len), cache->num_heads))
+        return HSTU_ERR_UNSUPPORTED;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    HSTU_CUDA(cudaMemsetAsync(workspace, 0, sizeof(WsHeader), st));
+    return cuda_status(launch_cache_append(c, bf16, k, k_stride, v, v_stride, new_lens, new_pos, st));
+}
+
+hstu_status hstu_cache_attn_workspace_size(const hstu_attn_desc *desc, const hstu_cache *cache,
+                                           int32_t max_cache_len, int32_t with_weights, size_t *bytes)
+{
+    HSTU_TRY(check_cache_attn(desc, cache, max_cache_len));
+    if (!bytes)
+        return HSTU_ERR_INVALID_ARG;
+    const CacheAttnPlan p = cache_attn_plan(cache_attn_call(desc, cache, max_cache_len), desc->dtype == HSTU_BF16,
+                                            with_weights != 0);
+    *bytes = sizeof(WsHeader) + p.part_o_bytes + p.part_w_bytes;
+    return HSTU_OK;
+}
+
+hstu_status hstu_cache_attn_fwd(const hstu_attn_desc *desc, const hstu_cache *cache, int32_t max_cache_len,
+                                const void *q, int64_t q_stride, const int64_t *seq_offsets,
+                                const int64_t *timestamps, const int32_t *num_targets, const float *rab_pos,
+                                const float *rab_time, const int32_t *block_table, const int32_t *cache_lens,
+                                const int32_t *seq_pos, const void *addend, float *weights_out, void *out,
+                                void *workspace, size_t workspace_bytes, void *stream)
+{
+    HSTU_TRY(check_cache_attn(desc, cache, max_cache_len));
+    if (!seq_offsets || !rab_pos || !rab_time)
+        return HSTU_ERR_INVALID_ARG;
+    if (desc->num_seqs > 0 && (!cache_lens || (cache->max_pages > 0 && !block_table)))
+        return HSTU_ERR_INVALID_ARG;
+    if (desc->total_tokens > 0 && (!q || !out || !timestamps))
+        return HSTU_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(out) || !aligned16(addend))
+        return HSTU_ERR_INVALID_ARG;
+    const int64_t width = (int64_t)desc->num_heads * desc->d_qk;
+    if (desc->total_tokens > 0 && !row_stride_ok(q_stride, width, elem_bytes(desc)))
+        return HSTU_ERR_INVALID_ARG;
+    CacheAttnArgs a{};
+    a.c = cache_attn_call(desc, cache, max_cache_len);
+    a.plan = cache_attn_plan(a.c, desc->dtype == HSTU_BF16, weights_out != nullptr);
+    HSTU_TRY(check_ws(workspace, workspace_bytes, sizeof(WsHeader) + a.plan.part_o_bytes + a.plan.part_w_bytes));
+    if (!cache_attn_grid_ok(a))
+        return HSTU_ERR_UNSUPPORTED;
+    a.c.seq_offsets = seq_offsets;
+    a.c.num_targets = num_targets;
+    a.c.ts = timestamps;
+    a.c.table = block_table;
+    a.c.cache_lens = cache_lens;
+    a.c.seq_pos = seq_pos;
+    a.c.hdr = static_cast<WsHeader *>(workspace);
+    a.q = q;
+    a.ldq = q_stride;
+    a.rab_pos = rab_pos;
+    a.rab_time = rab_time;
+    a.pos_hstride = desc->per_head_tables ? (int64_t)desc->pos_hi - desc->pos_lo + 1 : 0;
+    a.time_hstride = desc->per_head_tables ? desc->num_time_buckets : 0;
+    a.pos_lo = desc->pos_lo;
+    a.pos_hi = desc->pos_hi;
+    a.nb = desc->num_time_buckets;
+    a.cand_own = desc->cand_positions;
+    a.inv_n = desc->inv_n;
+    a.addend = addend;
+    a.out = out;
+    a.weights_out = weights_out;
+    char *cur = static_cast<char *>(workspace) + sizeof(WsHeader);
+    a.part_o = reinterpret_cast<float *>(cur);
+    a.part_w = weights_out ? reinterpret_cast<float *>(cur + a.plan.part_o_bytes) : nullptr;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    HSTU_CUDA(cudaMemsetAsync(workspace, 0, sizeof(WsHeader), st));
+    return cuda_status(launch_cache_attn(a, desc->dtype == HSTU_BF16, st));
+}
+
+hstu_status hstu_cache_evict_workspace_size(const hstu_cache *cache, int32_t num_seqs, int32_t max_cache_len,
+                                            int32_t keep, size_t *bytes)
+{
+    HSTU_TRY(check_cache(cache));
+    if (num_seqs < 0 || max_cache_len < 0 || keep < 1 || !bytes)
+        return HSTU_ERR_INVALID_ARG;
+    *bytes = sizeof(WsHeader) + (max_cache_len > keep ? sizeof(uint32_t) * (size_t)num_seqs * max_cache_len : 0);
+    return HSTU_OK;
+}
+
+hstu_status hstu_cache_evict(const hstu_cache *cache, int32_t num_seqs, int32_t max_cache_len, int32_t keep,
+                             int32_t first, int32_t recent, const int32_t *block_table,
+                             const int32_t *cache_lens, const int32_t *new_pages, int32_t *new_table,
+                             int32_t *new_lens, int32_t *kept, void *workspace, size_t workspace_bytes,
+                             void *stream)
+{
+    size_t need = 0;
+    HSTU_TRY(hstu_cache_evict_workspace_size(cache, num_seqs, max_cache_len, keep, &need));
+    if (first < 0 || recent < 0 || (cache->num_pages > 0 && !cache->weights))
+        return HSTU_ERR_INVALID_ARG;
+    if (num_seqs > 0 && (!cache_lens || !new_lens || !kept))
+        return HSTU_ERR_INVALID_ARG;
+    if (num_seqs > 0 && cache->max_pages > 0 && (!block_table || !new_pages || !new_table))
+        return HSTU_ERR_INVALID_ARG;
+    if (num_seqs > 0 && (new_lens == cache_lens || (new_table && (new_table == block_table || new_table == new_pages))))
+        return HSTU_ERR_INVALID_ARG;
+    HSTU_TRY(check_ws(workspace, workspace_bytes, need));
+    if (!grid_ok(num_seqs, (keep + (int64_t)HSTU_CACHE_PAGE - 1) / HSTU_CACHE_PAGE, cache->num_heads) &&
+        !grid_ok(num_seqs, cache->max_pages, cache->num_heads))
+        return HSTU_ERR_UNSUPPORTED;
+    const CacheCall c = cache_call(cache, num_seqs, max_cache_len, block_table, cache_lens, workspace);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    HSTU_CUDA(cudaMemsetAsync(workspace, 0, sizeof(WsHeader), st));
+    return cuda_status(launch_cache_evict(c, keep, first, recent, new_pages, new_table, new_lens, kept,
+                                          reinterpret_cast<uint32_t *>(static_cast<char *>(workspace) + sizeof(WsHeader)),
+                                          max_cache_len, st));
 }
 
 hstu_status hstu_check_device_flag(const void *workspace, int32_t *bits, void *stream)

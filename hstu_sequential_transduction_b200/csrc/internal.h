@@ -10,6 +10,24 @@ namespace hstu {
 struct WsHeader;
 struct AttnParams;
 
+// A call on the 8-bit cache: the pool and its pages, the call's jagged tokens
+// (none for the eviction: seq_offsets null) and the lengths behind the table.
+struct CacheCall {
+    uint8_t *k_codes, *v_codes;
+    float *k_scale, *v_scale;
+    int64_t *timestamps;
+    int32_t *positions;
+    float *weights;
+    int num_pages, H, d, max_pages;
+    int B, max_seq_len, max_cache_len;
+    int64_t T;
+    const int64_t *seq_offsets;
+    const int32_t *num_targets;
+    const int64_t *ts;  // [T] stamps of the call's tokens
+    const int32_t *table, *cache_lens, *seq_pos;
+    WsHeader *hdr;
+};
+
 // SM count and L2 size of the current device (cached per device).
 struct DeviceInfo {
     int sms = 148;
@@ -145,5 +163,44 @@ constexpr int kTruncateMaxSeqs = 12288;
 cudaError_t launch_jagged_truncate(const int64_t *off, const int32_t *nt, int B, int64_t T, int keep,
                                    int64_t row_bytes, const void *in, void *out, int64_t *out_off,
                                    cudaStream_t stream);
+
+// 8-bit cache: append of new tokens (k, v rows ldk, ldv elements apart).
+int cache_append_blocks(int max_seq_len);
+cudaError_t launch_cache_append(const CacheCall &c, bool bf16, const void *k, int64_t ldk, const void *v, int64_t ldv,
+                                int32_t *new_lens, int32_t *new_pos, cudaStream_t stream);
+
+// 8-bit cache: eviction.  kept [B, keep] receives the old indices (then -1);
+// keys [B, cap] is scratch.
+cudaError_t launch_cache_evict(const CacheCall &c, int keep, int first, int recent, const int32_t *new_pages,
+                               int32_t *new_table, int32_t *new_lens, int32_t *kept, uint32_t *keys, int64_t cap,
+                               cudaStream_t stream);
+
+// 8-bit cache: attention over the cache.  The key axis is cut into `nsplit` parts
+// of `split_pages` pages; each part's sums go to part_o [nsplit, T, H, d] (float32)
+// and, where weights are taken, each head's to part_w [planes, B, lcap], one plane
+// per (query tile, head); a second kernel joins them in a fixed order.
+struct CacheAttnPlan {
+    int nsplit, split_pages;
+    int qtiles;  // query tiles that have planes of their own
+    int64_t lcap;
+    size_t part_o_bytes, part_w_bytes;
+};
+struct CacheAttnArgs {
+    CacheCall c;
+    CacheAttnPlan plan;
+    const void *q;
+    int64_t ldq;
+    const float *rab_pos, *rab_time;
+    int64_t pos_hstride, time_hstride;
+    int pos_lo, pos_hi, nb, cand_own;
+    float inv_n;
+    const void *addend;
+    void *out;
+    float *weights_out;
+    float *part_o, *part_w;
+};
+CacheAttnPlan cache_attn_plan(const CacheCall &c, bool bf16, bool with_weights);
+bool cache_attn_grid_ok(const CacheAttnArgs &a);  // its launches stay below the grid limit
+cudaError_t launch_cache_attn(const CacheAttnArgs &a, bool bf16, cudaStream_t stream);
 
 }  // namespace hstu

@@ -30,7 +30,11 @@ EXPORTED = ["hstu_status_string", "hstu_version", "hstu_attn_workspace_size",
             "hstu_check_device_flag", "hstu_debug_bias_indices", "hstu_debug_schedule",
             "hstu_attn_fwd_noalloc", "hstu_layer_bwd_workspace_size", "hstu_layer_bwd",
             "hstu_jagged_truncate", "hstu_quantize_weight_e4m3", "hstu_quantize_rows_e4m3", "hstu_gemm_e4m3",
-            "hstu_e4m3_weight_bytes"]
+            "hstu_e4m3_weight_bytes", "hstu_cache_append_workspace_size", "hstu_cache_append",
+            "hstu_cache_attn_workspace_size", "hstu_cache_attn_fwd", "hstu_cache_evict_workspace_size",
+            "hstu_cache_evict"]
+# tokens of a page of the 8-bit key/value cache
+HSTU_CACHE_PAGE = 64
 
 
 class HstuError(RuntimeError):
@@ -52,6 +56,13 @@ class hstu_attn_desc(ctypes.Structure):
 class hstu_layer_desc(ctypes.Structure):
     _fields_ = [("attn", hstu_attn_desc), ("d_model", ctypes.c_int32), ("ln_eps", ctypes.c_float),
                 ("output_concat", ctypes.c_int32), ("fp8_projections", ctypes.c_int32)]
+
+
+class hstu_cache(ctypes.Structure):
+    _fields_ = [("num_pages", ctypes.c_int32), ("num_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("timestamps", ctypes.c_void_p),
+                ("positions", ctypes.c_void_p), ("weights", ctypes.c_void_p)]
 
 
 _lock = threading.Lock()
@@ -410,6 +421,250 @@ def hstu_jagged_truncate(seq_offsets, num_targets, keep: int, rows, *, out=None,
         ctypes.c_int32(B), ctypes.c_int64(T), ctypes.c_int32(keep), _ptr(seq_offsets), _ptr(num_targets),
         _ptr(rows), ctypes.c_int64(row_bytes), _ptr(out), _ptr(out_offsets), _stream(stream)))
     return out_offsets, out
+
+
+class HstuCache:
+    """The tensors of an 8-bit key/value cache (layouts in include/hstu.h): E4M3 codes
+    k_codes [pages, H, 64, d] and v_codes [pages, H, d, 64] (uint8), their scales
+    [pages, H] (float32), and per token timestamps (int64), positions (int32) and
+    optionally weights (float32), all [pages, 64] on one CUDA device."""
+
+    def __init__(self, k_codes, v_codes, k_scale, v_scale, timestamps, positions, weights=None):
+        pages, heads, page, d = k_codes.shape
+        if page != HSTU_CACHE_PAGE:
+            raise ValueError(f"k_codes has pages of {page} tokens, not {HSTU_CACHE_PAGE}")
+        for name, t, dtype, shape in (("k_codes", k_codes, torch.uint8, (pages, heads, page, d)),
+                                      ("v_codes", v_codes, torch.uint8, (pages, heads, d, page)),
+                                      ("k_scale", k_scale, torch.float32, (pages, heads)),
+                                      ("v_scale", v_scale, torch.float32, (pages, heads)),
+                                      ("timestamps", timestamps, torch.int64, (pages, page)),
+                                      ("positions", positions, torch.int32, (pages, page)),
+                                      ("weights", weights, torch.float32, (pages, page))):
+            if t is None:
+                continue
+            _dev(t, name, dtype)
+            if tuple(t.shape) != shape:
+                raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+            _same_device(t, name, k_codes.device)
+        self.k_codes, self.v_codes, self.k_scale, self.v_scale = k_codes, v_codes, k_scale, v_scale
+        self.timestamps, self.positions, self.weights = timestamps, positions, weights
+        self.num_pages, self.num_heads, self.head_dim = int(pages), int(heads), int(d)
+        self.device = k_codes.device
+
+    @classmethod
+    def empty(cls, num_pages: int, num_heads: int, head_dim: int, device, weights: bool = True) -> "HstuCache":
+        """A cache of num_pages pages, all zero."""
+        def z(shape, dtype):
+            return torch.zeros(shape, dtype=dtype, device=device)
+
+        pages, tokens = (num_pages, num_heads), (num_pages, HSTU_CACHE_PAGE)
+        return cls(z(pages + (HSTU_CACHE_PAGE, head_dim), torch.uint8), z(pages + (head_dim, HSTU_CACHE_PAGE), torch.uint8),
+                   z(pages, torch.float32), z(pages, torch.float32), z(tokens, torch.int64), z(tokens, torch.int32),
+                   z(tokens, torch.float32) if weights else None)
+
+    def struct(self, max_pages: int) -> hstu_cache:
+        """The C struct of these tensors with block tables of max_pages columns."""
+        return hstu_cache(self.num_pages, self.num_heads, self.head_dim, int(max_pages), self.k_codes.data_ptr(),
+                          self.v_codes.data_ptr(), self.k_scale.data_ptr(), self.v_scale.data_ptr(),
+                          self.timestamps.data_ptr(), self.positions.data_ptr(),
+                          0 if self.weights is None else self.weights.data_ptr())
+
+
+def _same_device(t, name, device):
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the cache on {device}")
+
+
+def _cache_ints(cache, block_table, **tensors):
+    """Checks the block table [B, max_pages] and the int32 tensors [B] beside it."""
+    _dev(block_table, "block_table", torch.int32)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [num_seqs, max_pages]")
+    _same_device(block_table, "block_table", cache.device)
+    B = block_table.shape[0]
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        _dev(t, name, torch.int32)
+        if t.numel() != B:
+            raise ValueError(f"{name} has {t.numel()} entries for {B} sequences")
+        _same_device(t, name, cache.device)
+    return B
+
+
+def _cache_rows(cache, name, t):
+    """Checks a [T, H, d] tensor whose rows may lie further apart than H * d; the row stride."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    H, d = cache.num_heads, cache.head_dim
+    if t.dim() != 3 or t.shape[1] != H or t.shape[2] != d:
+        raise ValueError(f"{name} must be [T, {H}, {d}], got {list(t.shape)}")
+    st = t.stride()
+    if t.numel() and (st[2] != 1 or (H > 1 and st[1] != d)):
+        raise ValueError(f"{name} must have dense rows")
+    _same_device(t, name, cache.device)
+    return st[0] if t.shape[0] > 1 else H * d
+
+
+def _cache_stream(cache, stream):
+    return _stream(torch.cuda.current_stream(cache.device) if stream is None else stream)
+
+
+def _cache_tokens(cache, B, T, seq_offsets, timestamps):
+    _dev(seq_offsets, "seq_offsets", torch.int64)
+    _dev(timestamps, "timestamps", torch.int64)
+    if seq_offsets.numel() != B + 1 or timestamps.numel() != T:
+        raise ValueError(f"seq_offsets needs {B + 1} entries and timestamps {T}")
+    _same_device(seq_offsets, "seq_offsets", cache.device)
+    _same_device(timestamps, "timestamps", cache.device)
+
+
+def _cache_workspace(cache, workspace, need):
+    if workspace is None:
+        return alloc_workspace(need, cache.device)
+    _same_device(workspace, "workspace", cache.device)
+    return workspace
+
+
+def hstu_cache_append_workspace_size() -> int:
+    n = ctypes.c_size_t(0)
+    _check("hstu_cache_append_workspace_size", load_library().hstu_cache_append_workspace_size(ctypes.byref(n)))
+    return n.value
+
+
+def hstu_cache_append(k, v, cache: HstuCache, block_table, cache_lens, seq_pos, seq_offsets, timestamps, num_targets, *,
+                      max_seq_len: int, new_lens=None, new_pos=None, workspace=None, stream=None):
+    """Append each sequence's history tokens to the cache: k, v [T, H, d] (rows may lie
+    further apart, as in a projection's output).  Returns (new_lens, new_pos) [B] int32;
+    seq_pos None means cache_lens (nothing was evicted before)."""
+    B = _cache_ints(cache, block_table, cache_lens=cache_lens, seq_pos=seq_pos, num_targets=num_targets,
+                    new_lens=new_lens, new_pos=new_pos)
+    sk, sv = _cache_rows(cache, "k", k), _cache_rows(cache, "v", v)
+    if v.dtype != k.dtype or v.shape != k.shape:
+        raise ValueError("k and v must have one type and shape")
+    _cache_tokens(cache, B, k.shape[0], seq_offsets, timestamps)
+    if new_lens is None:
+        new_lens = torch.empty_like(cache_lens)
+    if new_pos is None:
+        new_pos = torch.empty_like(cache_lens)
+    workspace = _cache_workspace(cache, workspace, 256)
+    with torch.cuda.device(cache.device):
+        _check("hstu_cache_append", load_library().hstu_cache_append(
+            ctypes.byref(cache.struct(block_table.shape[1])), _dtype_code(k), B, int(max_seq_len),
+            ctypes.c_int64(k.shape[0]), _ptr(k), ctypes.c_int64(sk), _ptr(v), ctypes.c_int64(sv), _ptr(seq_offsets),
+            _ptr(timestamps), _ptr(num_targets), _ptr(block_table), _ptr(cache_lens), _ptr(seq_pos), _ptr(new_lens),
+            _ptr(new_pos), _ptr(workspace), ctypes.c_size_t(workspace.numel()), _cache_stream(cache, stream)))
+    return new_lens, new_pos
+
+
+def _cache_attn_desc(q, block_table, rab_pos, rab_time, max_seq_len, inv_n, pos_lo, pos_hi, cand_own_index):
+    nb, per_head = _tables(rab_pos, rab_time, q.shape[1], pos_lo, pos_hi)
+    return make_attn_desc(block_table.shape[0], max_seq_len, q.shape[0], q.shape[1], q.shape[2], q.shape[2],
+                          _dtype_code(q), inv_n, pos_lo, pos_hi, nb, cand_own_index=cand_own_index,
+                          per_head_tables=per_head)
+
+
+def hstu_cache_attn_workspace_size(q, cache: HstuCache, block_table, rab_pos, rab_time, *, max_seq_len: int,
+                                   max_cache_len: int, inv_n: float, pos_lo: int, pos_hi: int,
+                                   cand_own_index: bool = False, weights: bool = False) -> int:
+    desc = _cache_attn_desc(q, block_table, rab_pos, rab_time, max_seq_len, inv_n, pos_lo, pos_hi, cand_own_index)
+    n = ctypes.c_size_t(0)
+    _check("hstu_cache_attn_workspace_size", load_library().hstu_cache_attn_workspace_size(
+        ctypes.byref(desc), ctypes.byref(cache.struct(block_table.shape[1])), int(max_cache_len), int(weights),
+        ctypes.byref(n)))
+    return n.value
+
+
+def hstu_cache_attn_fwd(q, cache: HstuCache, block_table, cache_lens, seq_pos, seq_offsets, timestamps, num_targets,
+                        rab_pos, rab_time, *, max_seq_len: int, max_cache_len: int, inv_n: float, pos_lo: int,
+                        pos_hi: int, addend=None, weights_out=None, out=None, workspace=None, stream=None,
+                        cand_own_index: bool = False):
+    """Attention of q [T, H, d] over the sequences' whole caches, plus `addend` [T, H, d]
+    (hstu_attn_fwd over the new tokens themselves; may be `out`).  weights_out
+    [pages, 64] float32 receives the cached tokens' accumulated attention weight; it
+    may be cache.weights."""
+    B = _cache_ints(cache, block_table, cache_lens=cache_lens, seq_pos=seq_pos, num_targets=num_targets)
+    sq = _cache_rows(cache, "q", q)
+    _cache_tokens(cache, B, q.shape[0], seq_offsets, timestamps)
+    for name, t in (("rab_pos", rab_pos), ("rab_time", rab_time)):
+        _dev(t, name, torch.float32)
+        _same_device(t, name, cache.device)
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    for name, t in (("addend", addend), ("out", out)):
+        if t is None:
+            continue
+        _dev(t, name, q.dtype)
+        if t.shape != q.shape:
+            raise ValueError(f"{name} must have q's shape")
+        _same_device(t, name, cache.device)
+    if weights_out is not None:
+        _dev(weights_out, "weights_out", torch.float32)
+        if tuple(weights_out.shape) != (cache.num_pages, HSTU_CACHE_PAGE):
+            raise ValueError("weights_out must be [pages, 64]")
+        _same_device(weights_out, "weights_out", cache.device)
+    desc = _cache_attn_desc(q, block_table, rab_pos, rab_time, max_seq_len, inv_n, pos_lo, pos_hi, cand_own_index)
+    pool = cache.struct(block_table.shape[1])
+    lib = load_library()
+    with torch.cuda.device(cache.device):
+        if workspace is None:
+            n = ctypes.c_size_t(0)
+            _check("hstu_cache_attn_workspace_size", lib.hstu_cache_attn_workspace_size(
+                ctypes.byref(desc), ctypes.byref(pool), int(max_cache_len), int(weights_out is not None),
+                ctypes.byref(n)))
+            workspace = alloc_workspace(n.value, q.device)
+        _same_device(workspace, "workspace", cache.device)
+        _check("hstu_cache_attn_fwd", lib.hstu_cache_attn_fwd(
+            ctypes.byref(desc), ctypes.byref(pool), int(max_cache_len), _ptr(q), ctypes.c_int64(sq),
+            _ptr(seq_offsets), _ptr(timestamps), _ptr(num_targets), _ptr(rab_pos), _ptr(rab_time), _ptr(block_table),
+            _ptr(cache_lens), _ptr(seq_pos), _ptr(addend), _ptr(weights_out), _ptr(out), _ptr(workspace),
+            ctypes.c_size_t(workspace.numel()), _cache_stream(cache, stream)))
+    return out
+
+
+def hstu_cache_evict_workspace_size(cache: HstuCache, block_table, *, keep: int, max_cache_len: int, first: int = 0,
+                                    recent: int = 0) -> int:
+    n = ctypes.c_size_t(0)
+    _check("hstu_cache_evict_workspace_size", load_library().hstu_cache_evict_workspace_size(
+        ctypes.byref(cache.struct(block_table.shape[1])), block_table.shape[0], int(max_cache_len), int(keep),
+        ctypes.byref(n)))
+    return n.value
+
+
+def hstu_cache_evict(cache: HstuCache, block_table, cache_lens, new_pages, *, keep: int, max_cache_len: int,
+                     first: int = 0, recent: int = 0, new_table=None, new_lens=None, kept=None, workspace=None,
+                     stream=None):
+    """Cut every sequence of more than `keep` tokens to its first `first`, its last
+    `recent` and, of the rest, the tokens of largest weight; they move into the pages
+    of new_pages [B, max_pages].  Returns (new_table, new_lens, kept [B, keep])."""
+    B = _cache_ints(cache, block_table, cache_lens=cache_lens, new_lens=new_lens)
+    if cache.weights is None:
+        raise ValueError("eviction needs the cache's weights")
+    for name, t in (("new_pages", new_pages), ("new_table", new_table)):
+        if t is None:
+            continue
+        _dev(t, name, torch.int32)
+        if t.shape != block_table.shape:
+            raise ValueError(f"{name} must have block_table's shape")
+        _same_device(t, name, cache.device)
+    need = hstu_cache_evict_workspace_size(cache, block_table, keep=keep, max_cache_len=max_cache_len)
+    if new_table is None:
+        new_table = torch.empty_like(block_table)
+    if new_lens is None:
+        new_lens = torch.empty_like(cache_lens)
+    if kept is None:
+        kept = torch.empty((B, int(keep)), dtype=torch.int32, device=cache.device)
+    _dev(kept, "kept", torch.int32)
+    if tuple(kept.shape) != (B, int(keep)):
+        raise ValueError(f"kept must be [{B}, {keep}]")
+    _same_device(kept, "kept", cache.device)
+    workspace = _cache_workspace(cache, workspace, need)
+    with torch.cuda.device(cache.device):
+        _check("hstu_cache_evict", load_library().hstu_cache_evict(
+            ctypes.byref(cache.struct(block_table.shape[1])), B, int(max_cache_len), int(keep), int(first),
+            int(recent), _ptr(block_table), _ptr(cache_lens), _ptr(new_pages), _ptr(new_table), _ptr(new_lens),
+            _ptr(kept), _ptr(workspace), ctypes.c_size_t(workspace.numel()), _cache_stream(cache, stream)))
+    return new_table, new_lens, kept
 
 
 def hstu_check_device_flag(workspace: torch.Tensor, stream=None):

@@ -288,6 +288,131 @@ hstu_status hstu_gemm_e4m3(const void *codes, const float *scales, int64_t M, in
                            size_t workspace_bytes, void *stream);
 
 /*
+ * 8-bit key/value cache.  A serving program keeps each user's history as pages
+ * of 64 tokens instead of recomputing it.  Since the attention is pointwise
+ * (no softmax), the attention of new tokens is the sum of two calls: over the
+ * new tokens themselves (hstu_attn_fwd) and over the cached history
+ * (hstu_cache_attn_fwd, whose `addend` takes the first one's output).
+ *
+ *   k_codes    uint8 [num_pages, H, 64, d]   E4M3 codes of the keys
+ *   v_codes    uint8 [num_pages, H, d, 64]   E4M3 codes of the values, transposed
+ *   k_scale, v_scale  float32 [num_pages, H]; a stored value is code * scale
+ *   timestamps int64 [num_pages, 64], positions int32 [num_pages, 64]
+ *   weights    float32 [num_pages, 64] attention weight each token received so
+ *              far, or NULL
+ * All of them are the caller's device memory; codes 16-byte aligned.  Page
+ * p of sequence b is block_table[b * max_pages + p] (int32, device); its token j
+ * sits in slot j % 64 of page j / 64.  cache_lens int32 [B] (device) counts a
+ * sequence's cached tokens, seq_pos int32 [B] (device) the tokens it has ever
+ * had, which is the position of its next one; NULL: the same as cache_lens
+ * (nothing was evicted).
+ *
+ * Scale of a block (page and head): the smallest power of two 2^e, e >= -126,
+ * with amax <= 448 * 2^e; 0 if every value is zero; NaN if a value is not
+ * finite (the block's values are then all NaN).  Powers of two divide exactly,
+ * so a code is the value's one rounding to E4M3 (nearest even), and a block
+ * whose scale grows shifts its older codes (rounding again only those that
+ * leave E4M3's normal range).
+ *
+ * Device checks add two bits to those of hstu_check_device_flag:
+ * 64 = cache_lens outside [0, max_cache_len] or the table's room, or tokens
+ * that do not fit: the sequence is dropped; 128 = a page outside the pool: its
+ * tokens are skipped.  Nothing is read or written out of range.
+ */
+#define HSTU_CACHE_PAGE 64
+
+typedef struct {
+    int32_t num_pages;  /* pages of the pool */
+    int32_t num_heads;  /* H */
+    int32_t head_dim;   /* d */
+    int32_t max_pages;  /* columns of a block table */
+    uint8_t *k_codes, *v_codes;
+    float *k_scale, *v_scale;
+    int64_t *timestamps;
+    int32_t *positions;
+    float *weights;
+} hstu_cache;
+
+/* Bytes of device workspace hstu_cache_append needs. */
+hstu_status hstu_cache_append_workspace_size(size_t *bytes);
+
+/*
+ * Append each sequence's history tokens (all but its last num_targets[b], which
+ * are candidates) to the cache.  k, v: [total_tokens, H, d] of `dtype`, rows
+ * k_stride and v_stride elements apart (multiples of 16 bytes; H * d where
+ * dense), 16-byte aligned; d is 64 or 128 for HSTU_BF16, 32 or 64 for HSTU_F32.
+ * Token i of the call gets position seq_pos[b] + i and weight 0.  new_lens
+ * (cache_lens + appended) and new_pos (seq_pos + appended, may be NULL) are
+ * int32 [B] and must not overlap cache_lens and seq_pos.  A dropped sequence
+ * keeps its length.  The pages a call writes must belong to one sequence each;
+ * slots behind a sequence's last token keep their bytes.
+ */
+hstu_status hstu_cache_append(const hstu_cache *cache, int32_t dtype, int32_t num_seqs, int32_t max_seq_len,
+                              int64_t total_tokens, const void *k, int64_t k_stride, const void *v,
+                              int64_t v_stride, const int64_t *seq_offsets, const int64_t *timestamps,
+                              const int32_t *num_targets, const int32_t *block_table, const int32_t *cache_lens,
+                              const int32_t *seq_pos, int32_t *new_lens, int32_t *new_pos, void *workspace,
+                              size_t workspace_bytes, void *stream);
+
+/* Bytes of device workspace hstu_cache_attn_fwd needs. */
+hstu_status hstu_cache_attn_workspace_size(const hstu_attn_desc *desc, const hstu_cache *cache,
+                                           int32_t max_cache_len, int32_t with_weights, size_t *bytes);
+
+/*
+ * Attention of a call's tokens over their sequences' whole caches:
+ *   s_ij  = q_i . k_j + rab_pos[p_i - p_j] + rab_time[bucket(t_i - t_j)]
+ *   out_i = inv_n * sum_j SiLU(s_ij) v_j + addend_i
+ *   weights_out_j = weights_j + inv_n * sum over heads and i of |SiLU(s_ij)|
+ * j runs over the cache_lens[b] cached tokens of i's sequence, all of them
+ * visible; p_j and t_j are the cached ones, p_i = seq_pos[b] + i for history
+ * tokens and seq_pos[b] + L_b - n_t (+ own index with cand_positions) for
+ * candidates.  Biases, clamps and tables as in hstu_attn_fwd.  A sequence with
+ * an empty cache gets its addend, or zeros.
+ *   desc       the call's tokens; fp8_qk, debug_checks and the windows must be 0
+ *   max_cache_len >= every cache_lens[b]; sizes the launch and the workspace
+ *   q          [T, H, d], rows q_stride elements apart, 16-byte aligned
+ *   addend     [T, H, d] of q's type or NULL; may be `out`
+ *   weights_out float32 [num_pages, 64] or NULL; may be cache->weights, and
+ *              starts from 0 where that is NULL.  Only the cached tokens of the
+ *              call's sequences are written; with weights_out these sequences
+ *              must not share pages.
+ * float32 q is computed to float32 accuracy; for bf16 q, products are exact and
+ * sums float32, and P is rounded to 16 bits before P V.
+ */
+hstu_status hstu_cache_attn_fwd(const hstu_attn_desc *desc, const hstu_cache *cache, int32_t max_cache_len,
+                                const void *q, int64_t q_stride, const int64_t *seq_offsets,
+                                const int64_t *timestamps, const int32_t *num_targets, const float *rab_pos,
+                                const float *rab_time, const int32_t *block_table, const int32_t *cache_lens,
+                                const int32_t *seq_pos, const void *addend, float *weights_out, void *out,
+                                void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of device workspace hstu_cache_evict needs. */
+hstu_status hstu_cache_evict_workspace_size(const hstu_cache *cache, int32_t num_seqs, int32_t max_cache_len,
+                                            int32_t keep, size_t *bytes);
+
+/*
+ * Eviction by accumulated attention weight.  A sequence of more than `keep`
+ * tokens keeps its last min(recent, keep) tokens, of the others the first
+ * `first` (as far as they fit), and of the rest those of largest weight (ties
+ * to the lower index, NaN below every number) up to `keep`, in order; they move
+ * with their stamps, positions and weights into the pages of its row of
+ * new_pages [B, max_pages] (the first ceil(keep / 64) entries are written),
+ * each block with a scale of its own.  A shorter sequence stays where it is.
+ *   new_table [B, max_pages]  the row of new_pages of a sequence that moved,
+ *                             else of block_table
+ *   new_lens  [B]             min(cache_lens[b], keep)
+ *   kept      [B, keep] int32 the kept tokens' old indices, then -1
+ * new_table, new_lens and kept must not overlap the inputs, and the pages that
+ * are written must belong to no sequence and occur once.  Old pages are left as
+ * they were.  keep >= 1, first >= 0, recent >= 0, cache->weights given.
+ */
+hstu_status hstu_cache_evict(const hstu_cache *cache, int32_t num_seqs, int32_t max_cache_len, int32_t keep,
+                             int32_t first, int32_t recent, const int32_t *block_table,
+                             const int32_t *cache_lens, const int32_t *new_pages, int32_t *new_table,
+                             int32_t *new_lens, int32_t *kept, void *workspace, size_t workspace_bytes,
+                             void *stream);
+
+/*
  * Attention forward that allocates nothing (no counterpart on the HSTU
  * pages; it exists for callers, not for the method).  Same computation,
  * arguments and layouts as hstu_attn_fwd, without the workspace: some callers
@@ -316,7 +441,8 @@ hstu_status hstu_attn_fwd_noalloc(const hstu_attn_desc *desc, const void *q, con
  * flag's bits (1 = seq_offsets[0] != 0, 2 = a sequence decreasing or past T,
  * 4 = a sequence longer than max_seq_len, 8 = num_targets outside [0, L_b],
  * 16 = seq_offsets[B] != T, 32 = a pipeline wait of a tcgen05 kernel ran
- * out: the kernel gave up instead of hanging, and its output is incomplete)
+ * out: the kernel gave up instead of hanging, and its output is incomplete;
+ * 64, 128 = the 8-bit cache's, above)
  * are stored in *bits when bits is not NULL.
  */
 hstu_status hstu_check_device_flag(const void *workspace, int32_t *bits, void *stream);
