@@ -197,9 +197,13 @@ template <typename T, int D>
 cudaError_t attn(const CacheAttnArgs &a, cudaStream_t stream)
 {
     const int64_t grid = (int64_t)a.c.B * a.plan.qtiles * a.c.H * a.plan.nsplit;
-    if (grid > 0)
+    cudaError_t e = cudaSuccess;
+    if (grid > 0 && a.plan.rows) {
+        e = launch_cache_attn_rows(a, stream);
+    } else if (grid > 0) {
         cache_attn_kernel<T, D><<<(unsigned)grid, kThreads, 0, stream>>>(a);
-    const cudaError_t e = cudaGetLastError();
+        e = cudaGetLastError();
+    }
     return e != cudaSuccess ? e : join<T>(a, stream);
 }
 
@@ -207,14 +211,19 @@ cudaError_t attn(const CacheAttnArgs &a, cudaStream_t stream)
 
 CacheAttnPlan cache_attn_plan(const CacheCall &c, bool bf16, bool with_weights)
 {
-    (void)bf16;
     CacheAttnPlan p{};
     const int64_t pages = (c.max_cache_len + kPage - 1) / kPage;
+    p.rows = bf16 && c.max_seq_len <= kCacheRows;
+    p.tile_rows = kRows;
     p.qtiles = (c.max_seq_len + kRows - 1) / kRows;
     const int64_t units = std::max<int64_t>(1, (int64_t)c.B * c.H * p.qtiles);
     // enough CTAs for four rounds of the SMs, each with one page at least
-    const int64_t want = std::max<int64_t>(1, std::min<int64_t>(pages, (4LL * device_info().sms + units - 1) / units));
+    int64_t want = std::max<int64_t>(1, std::min<int64_t>(pages, (4LL * device_info().sms + units - 1) / units));
     p.split_pages = (int)std::max<int64_t>(1, (pages + want - 1) / want);
+    if (p.rows) {
+        want = (16LL * device_info().sms + units - 1) / units;
+        p.split_pages = (int)std::max<int64_t>(4, (pages + want - 1) / want);
+    }
     p.nsplit = (int)((pages + p.split_pages - 1) / p.split_pages);
     p.lcap = pages * kPage;
     p.part_o_bytes = align256(sizeof(float) * (size_t)p.nsplit * c.T * c.H * c.d);

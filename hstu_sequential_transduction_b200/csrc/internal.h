@@ -179,8 +179,11 @@ cudaError_t launch_cache_evict(const CacheCall &c, int keep, int first, int rece
 // of `split_pages` pages; each part's sums go to part_o [nsplit, T, H, d] (float32)
 // and, where weights are taken, each head's to part_w [planes, B, lcap], one plane
 // per (query tile, head); a second kernel joins them in a fixed order.
+constexpr int kCacheRows = 16;  // query rows up to which the few-rows kernel runs (bf16)
 struct CacheAttnPlan {
+    bool rows;  // the few-rows kernel
     int nsplit, split_pages;
+    int tile_rows;
     int qtiles;  // query tiles that have planes of their own
     int64_t lcap;
     size_t part_o_bytes, part_w_bytes;
@@ -199,6 +202,7 @@ struct CacheAttnArgs {
     float *weights_out;
     float *part_o, *part_w;
 };
+cudaError_t launch_cache_attn_rows(const CacheAttnArgs &a, cudaStream_t stream);
 CacheAttnPlan cache_attn_plan(const CacheCall &c, bool bf16, bool with_weights);
 bool cache_attn_grid_ok(const CacheAttnArgs &a);  // its launches stay below the grid limit
 cudaError_t launch_cache_attn(const CacheAttnArgs &a, bool bf16, cudaStream_t stream);
