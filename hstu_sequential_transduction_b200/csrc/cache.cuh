@@ -61,6 +61,24 @@ __device__ __forceinline__ int table_page(const int32_t *table, const CacheCall 
     return page >= 0 && page < c.num_pages ? page : -1;
 }
 
+// weights_out of cached token j of sequence b: what it had plus its planes, in order.
+__device__ __forceinline__ void cache_join_weight(const CacheAttnArgs &a, int b, int j)
+{
+    const CacheCall &c = a.c;
+    const CacheSeq s = cache_seq(c, b);
+    if (j >= s.len)
+        return;
+    const int page = table_page(c.table, c, b, j / kPage);
+    if (page < 0)
+        return;
+    const int planes = (s.n + a.plan.tile_rows - 1) / a.plan.tile_rows * c.H;
+    float sum = 0.f;
+    for (int p = 0; p < planes; p++)
+        sum += a.part_w[((int64_t)p * c.B + b) * a.plan.lcap + j];
+    const int64_t at = (int64_t)page * kPage + j % kPage;
+    a.weights_out[at] = fmaf(fabsf(a.inv_n), sum, c.weights ? c.weights[at] : 0.f);
+}
+
 // ---- E4M3 ---------------------------------------------------------------------
 
 // two codes (low 16 bits) to two f16: exact

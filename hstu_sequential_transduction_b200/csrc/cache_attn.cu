@@ -1,5 +1,5 @@
-// Attention over the 8-bit key/value cache on CUDA cores, and the join of the
-// parts that the key axis is cut into.
+// Attention over the 8-bit key/value cache: the float32 kernel (CUDA cores), the join
+// of the parts that the key axis is cut into, and the choice of kernel.
 //
 //   O_i = inv_n sum_j SiLU(q_i . k_j + bias_ij) v_j,   a_j += |inv_n| sum_ih |SiLU|
 //
@@ -33,9 +33,9 @@ __device__ __forceinline__ void decode16(const uint4 w, float *x)
     }
 }
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads)
-cache_attn_kernel(const CacheAttnArgs a)
+cache_attn_f32_kernel(const CacheAttnArgs a)
 {
     constexpr int RG = kThreads / D;       // row groups of the value product
     constexpr int NR = kRows / RG;
@@ -50,18 +50,13 @@ cache_attn_kernel(const CacheAttnArgs a)
     const int tile = x % a.plan.qtiles, b = x / a.plan.qtiles;
     const int tid = threadIdx.x;
     const CacheSeq s = cache_seq(c, b);
-    if (s.bits) {
-        if (part == 0 && h == 0 && tile == 0 && tid == 0)
-            atomicOr(&c.hdr->flag, s.bits);
-        return;
-    }
     const int r0 = tile * kRows, rows = min(s.n - r0, kRows);
     const int p0 = part * a.plan.split_pages, p1 = min((s.len + kPage - 1) / kPage, p0 + a.plan.split_pages);
     if (rows <= 0 || p0 >= p1)
         return;
-    const T *q = static_cast<const T *>(a.q);
+    const float *q = static_cast<const float *>(a.q);
     for (int i = tid; i < kRows * D; i += kThreads)
-        sq[i / D][i % D] = i / D < rows ? to_float(q[(s.s0 + r0 + i / D) * a.ldq + (int64_t)h * D + i % D]) : 0.f;
+        sq[i / D][i % D] = i / D < rows ? (q[(s.s0 + r0 + i / D) * a.ldq + (int64_t)h * D + i % D]) : 0.f;
     const float *rp = a.rab_pos + h * a.pos_hstride, *rt = a.rab_time + h * a.time_hstride;
     const int key = tid % kPage, half = tid / kPage;
     const int dim = tid % D, rg = tid / D;
@@ -138,16 +133,18 @@ cache_attn_kernel(const CacheAttnArgs a)
 __device__ __forceinline__ void put(float *p, float x) { *p = x; }
 __device__ __forceinline__ void put(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
 
-// Adds the parts: blocks [0, row_blocks) the output's rows, the others the weights.
+// Adds the parts: blocks [0, row_blocks * B) the output's rows, the others the weights.
 template <typename T>
 __global__ void __launch_bounds__(256)
-cache_join_kernel(const CacheAttnArgs a, int row_blocks, int w_blocks, int tile_rows)
+cache_join_kernel(const CacheAttnArgs a, int row_blocks, int w_blocks)
 {
     const CacheCall &c = a.c;
     const int64_t width = (int64_t)c.H * c.d;
     if ((int64_t)blockIdx.x < (int64_t)row_blocks * c.B) {
         const int b = blockIdx.x / row_blocks, chunk = blockIdx.x % row_blocks;
         const CacheSeq s = cache_seq(c, b);
+        if (s.bits && chunk == 0 && threadIdx.x == 0)
+            atomicOr(&c.hdr->flag, s.bits);
         const int nsp = ((s.len + kPage - 1) / kPage + a.plan.split_pages - 1) / a.plan.split_pages;
         const int64_t at = (int64_t)chunk * 1024 + threadIdx.x, end = (int64_t)s.n * width;
         T *out = static_cast<T *>(a.out);
@@ -165,46 +162,21 @@ cache_join_kernel(const CacheAttnArgs a, int row_blocks, int w_blocks, int tile_
         return;
     }
     const int x = blockIdx.x - row_blocks * c.B;
-    const int b = x / w_blocks, j = (x % w_blocks) * 256 + threadIdx.x;
-    const CacheSeq s = cache_seq(c, b);
-    if (j >= s.len)
-        return;
-    const int page = table_page(c.table, c, b, j / kPage);
-    if (page < 0)
-        return;
-    const int planes = (s.n + tile_rows - 1) / tile_rows * c.H;
-    float sum = 0.f;
-    for (int p = 0; p < planes; p++)
-        sum += a.part_w[((int64_t)p * c.B + b) * a.plan.lcap + j];
-    const int64_t at = (int64_t)page * kPage + j % kPage;
-    a.weights_out[at] = fmaf(fabsf(a.inv_n), sum, c.weights ? c.weights[at] : 0.f);
+    cache_join_weight(a, x / w_blocks, (x % w_blocks) * 256 + threadIdx.x);
+}
+
+int row_blocks(const CacheCall &c)  // one at least: it reports a sequence that was dropped
+{
+    return (int)std::max<int64_t>(1, ((int64_t)c.max_seq_len * c.H * c.d + 1023) / 1024);
 }
 
 template <typename T>
 cudaError_t join(const CacheAttnArgs &a, cudaStream_t stream)
 {
     const CacheCall &c = a.c;
-    const int row_blocks = (int)(((int64_t)c.max_seq_len * c.H * c.d + 1023) / 1024);
-    const int w_blocks = a.weights_out ? (c.max_cache_len + 255) / 256 : 0;
-    const int64_t grid = (int64_t)(row_blocks + w_blocks) * c.B;
-    if (grid == 0)
-        return cudaSuccess;
-    cache_join_kernel<T><<<(unsigned)grid, 256, 0, stream>>>(a, row_blocks, w_blocks, kRows);
+    const int rows = row_blocks(c), w_blocks = a.weights_out ? (c.max_cache_len + 255) / 256 : 0;
+    cache_join_kernel<T><<<(unsigned)((rows + w_blocks) * c.B), 256, 0, stream>>>(a, rows, w_blocks);
     return cudaGetLastError();
-}
-
-template <typename T, int D>
-cudaError_t attn(const CacheAttnArgs &a, cudaStream_t stream)
-{
-    const int64_t grid = (int64_t)a.c.B * a.plan.qtiles * a.c.H * a.plan.nsplit;
-    cudaError_t e = cudaSuccess;
-    if (grid > 0 && a.plan.rows) {
-        e = launch_cache_attn_rows(a, stream);
-    } else if (grid > 0) {
-        cache_attn_kernel<T, D><<<(unsigned)grid, kThreads, 0, stream>>>(a);
-        e = cudaGetLastError();
-    }
-    return e != cudaSuccess ? e : join<T>(a, stream);
 }
 
 }  // namespace
@@ -213,38 +185,59 @@ CacheAttnPlan cache_attn_plan(const CacheCall &c, bool bf16, bool with_weights)
 {
     CacheAttnPlan p{};
     const int64_t pages = (c.max_cache_len + kPage - 1) / kPage;
-    p.rows = bf16 && c.max_seq_len <= kCacheRows;
-    p.tile_rows = kRows;
-    p.qtiles = (c.max_seq_len + kRows - 1) / kRows;
-    const int64_t units = std::max<int64_t>(1, (int64_t)c.B * c.H * p.qtiles);
-    // enough CTAs for four rounds of the SMs, each with one page at least
-    int64_t want = std::max<int64_t>(1, std::min<int64_t>(pages, (4LL * device_info().sms + units - 1) / units));
-    p.split_pages = (int)std::max<int64_t>(1, (pages + want - 1) / want);
-    if (p.rows) {
-        want = (16LL * device_info().sms + units - 1) / units;
-        p.split_pages = (int)std::max<int64_t>(4, (pages + want - 1) / want);
-    }
-    p.nsplit = (int)((pages + p.split_pages - 1) / p.split_pages);
+    const int64_t sms = device_info().sms;
+    p.kernel = !bf16 ? CACHE_F32 : c.max_seq_len <= kCacheRows ? CACHE_ROWS : CACHE_TC;
+    p.tile_rows = p.kernel == CACHE_TC ? kTcTile : kRows;
+    p.qtiles = (c.max_seq_len + p.tile_rows - 1) / p.tile_rows;
     p.lcap = pages * kPage;
-    p.part_o_bytes = align256(sizeof(float) * (size_t)p.nsplit * c.T * c.H * c.d);
+    const int64_t units = (int64_t)c.B * c.H * p.qtiles;
+    if (units > 0 && pages > 0 && p.kernel == CACHE_TC) {
+        p.ctas = (int)std::min<int64_t>(sms, units * ((pages + 1) / 2));
+        p.part_o_bytes = align256(sizeof(float) * 2 * p.ctas * (size_t)kTcTile * c.d);
+        p.piece_bytes = align256(sizeof(CacheAttnPiece) * 2 * p.ctas);
+    } else {
+        // rows: a warp should have several pages to keep its loads going, but with few
+        // units the pages spread over the SMs; float32: four rounds of the SMs
+        const int64_t want = std::max<int64_t>(1, ((p.kernel == CACHE_ROWS ? 16 : 4) * sms + units - 1) / std::max<int64_t>(1, units));
+        p.split_pages = (int)std::max<int64_t>(p.kernel == CACHE_ROWS ? 4 : 1, (pages + want - 1) / want);
+        p.nsplit = (int)((pages + p.split_pages - 1) / p.split_pages);
+        p.part_o_bytes = align256(sizeof(float) * (size_t)p.nsplit * c.T * c.H * c.d);
+    }
     p.part_w_bytes = with_weights ? align256(sizeof(float) * (size_t)p.qtiles * c.H * c.B * p.lcap) : 0;
     return p;
 }
 
-bool cache_attn_grid_ok(const CacheAttnArgs &a)
+bool cache_attn_fits(const CacheAttnArgs &a)
 {
-    const double row_blocks = (double)a.c.max_seq_len * a.c.H * a.c.d / 1024 + 1;
-    return (double)a.c.B * a.plan.qtiles * a.c.H * a.plan.nsplit < 2147483647.0 &&
-           (row_blocks + a.plan.lcap / 256 + 1) * a.c.B < 2147483647.0;
+    const CacheCall &c = a.c;
+    const double limit = 2147483647.0;
+    const double w_blocks = (double)(a.plan.lcap / 256 + 1) * c.B;
+    if (a.plan.kernel == CACHE_TC)  // TMA coordinates: rows of the pool's codes
+        return (double)c.num_pages * c.H * kPage < limit && w_blocks + c.B + 4.0 * a.plan.ctas < limit;
+    return (double)c.B * a.plan.qtiles * c.H * a.plan.nsplit < limit &&
+           ((double)c.max_seq_len * c.H * c.d / 1024 + 2) * c.B + w_blocks < limit;
 }
 
 cudaError_t launch_cache_attn(const CacheAttnArgs &a, bool bf16, cudaStream_t stream)
 {
     if (a.c.B == 0)
         return cudaSuccess;
-    if (bf16)
-        return a.c.d == 64 ? attn<__nv_bfloat16, 64>(a, stream) : attn<__nv_bfloat16, 128>(a, stream);
-    return a.c.d == 32 ? attn<float, 32>(a, stream) : attn<float, 64>(a, stream);
+    if (a.plan.kernel == CACHE_TC)
+        return launch_cache_attn_tc(a, stream);
+    const int64_t grid = (int64_t)a.c.B * a.plan.qtiles * a.c.H * a.plan.nsplit;
+    cudaError_t e = cudaSuccess;
+    if (grid > 0 && a.plan.kernel == CACHE_ROWS) {
+        e = launch_cache_attn_rows(a, stream);
+    } else if (grid > 0) {
+        if (a.c.d == 32)
+            cache_attn_f32_kernel<32><<<(unsigned)grid, kThreads, 0, stream>>>(a);
+        else
+            cache_attn_f32_kernel<64><<<(unsigned)grid, kThreads, 0, stream>>>(a);
+        e = cudaGetLastError();
+    }
+    if (e != cudaSuccess)
+        return e;
+    return bf16 ? join<__nv_bfloat16>(a, stream) : join<float>(a, stream);
 }
 
 }  // namespace hstu

@@ -77,11 +77,6 @@ cache_attn_rows_kernel(const CacheAttnArgs a)
     const int part = x % a.plan.nsplit, b = x / a.plan.nsplit;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const CacheSeq s = cache_seq(c, b);
-    if (s.bits) {
-        if (part == 0 && h == 0 && threadIdx.x == 0)
-            atomicOr(&c.hdr->flag, s.bits);
-        return;
-    }
     const int rows = s.n;  // at most R: the launch is chosen by max_seq_len
     const int p0 = part * a.plan.split_pages, p1 = min((s.len + kPage - 1) / kPage, p0 + a.plan.split_pages);
     if (rows == 0 || p0 >= p1)

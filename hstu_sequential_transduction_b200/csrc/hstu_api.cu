@@ -234,14 +234,14 @@ hstu_status attn_bwd_strided(const hstu_attn_desc *desc, const void *q, int64_t 
 
 hstu_status check_cache(const hstu_cache *c)
 {
-    if (!c || c->num_pages < 0 || c->num_heads < 1 || c->max_pages < 0)
+    if (!c || c->num_pages < 1 || c->num_heads < 1 || c->max_pages < 0)
         return HSTU_ERR_INVALID_ARG;
     if (c->head_dim != 32 && c->head_dim != 64 && c->head_dim != 128)
         return HSTU_ERR_UNSUPPORTED;
     if ((int64_t)c->max_pages * HSTU_CACHE_PAGE > INT_MAX)
         return HSTU_ERR_UNSUPPORTED;
-    if (c->num_pages > 0 && (!c->k_codes || !c->v_codes || !c->k_scale || !c->v_scale || !c->timestamps ||
-                             !c->positions || !aligned16(c->k_codes) || !aligned16(c->v_codes)))
+    if (!c->k_codes || !c->v_codes || !c->k_scale || !c->v_scale || !c->timestamps || !c->positions ||
+        !aligned16(c->k_codes) || !aligned16(c->v_codes))
         return HSTU_ERR_INVALID_ARG;
     return HSTU_OK;
 }
@@ -839,7 +839,7 @@ hstu_status hstu_cache_attn_workspace_size(const hstu_attn_desc *desc, const hst
         return HSTU_ERR_INVALID_ARG;
     const CacheAttnPlan p = cache_attn_plan(cache_attn_call(desc, cache, max_cache_len), desc->dtype == HSTU_BF16,
                                             with_weights != 0);
-    *bytes = sizeof(WsHeader) + p.part_o_bytes + p.part_w_bytes;
+    *bytes = sizeof(WsHeader) + p.part_o_bytes + p.part_w_bytes + p.piece_bytes;
     return HSTU_OK;
 }
 
@@ -865,8 +865,8 @@ hstu_status hstu_cache_attn_fwd(const hstu_attn_desc *desc, const hstu_cache *ca
     CacheAttnArgs a{};
     a.c = cache_attn_call(desc, cache, max_cache_len);
     a.plan = cache_attn_plan(a.c, desc->dtype == HSTU_BF16, weights_out != nullptr);
-    HSTU_TRY(check_ws(workspace, workspace_bytes, sizeof(WsHeader) + a.plan.part_o_bytes + a.plan.part_w_bytes));
-    if (!cache_attn_grid_ok(a))
+    HSTU_TRY(check_ws(workspace, workspace_bytes, sizeof(WsHeader) + a.plan.part_o_bytes + a.plan.part_w_bytes + a.plan.piece_bytes));
+    if (!cache_attn_fits(a))
         return HSTU_ERR_UNSUPPORTED;
     a.c.seq_offsets = seq_offsets;
     a.c.num_targets = num_targets;
@@ -892,6 +892,7 @@ hstu_status hstu_cache_attn_fwd(const hstu_attn_desc *desc, const hstu_cache *ca
     char *cur = static_cast<char *>(workspace) + sizeof(WsHeader);
     a.part_o = reinterpret_cast<float *>(cur);
     a.part_w = weights_out ? reinterpret_cast<float *>(cur + a.plan.part_o_bytes) : nullptr;
+    a.pieces = reinterpret_cast<CacheAttnPiece *>(cur + a.plan.part_o_bytes + a.plan.part_w_bytes);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     HSTU_CUDA(cudaMemsetAsync(workspace, 0, sizeof(WsHeader), st));
     return cuda_status(launch_cache_attn(a, desc->dtype == HSTU_BF16, st));
@@ -915,7 +916,7 @@ hstu_status hstu_cache_evict(const hstu_cache *cache, int32_t num_seqs, int32_t 
 {
     size_t need = 0;
     HSTU_TRY(hstu_cache_evict_workspace_size(cache, num_seqs, max_cache_len, keep, &need));
-    if (first < 0 || recent < 0 || (cache->num_pages > 0 && !cache->weights))
+    if (first < 0 || recent < 0 || !cache->weights)
         return HSTU_ERR_INVALID_ARG;
     if (num_seqs > 0 && (!cache_lens || !new_lens || !kept))
         return HSTU_ERR_INVALID_ARG;

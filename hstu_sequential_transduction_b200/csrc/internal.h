@@ -175,18 +175,26 @@ cudaError_t launch_cache_evict(const CacheCall &c, int keep, int first, int rece
                                int32_t *new_table, int32_t *new_lens, int32_t *kept, uint32_t *keys, int64_t cap,
                                cudaStream_t stream);
 
-// 8-bit cache: attention over the cache.  The key axis is cut into `nsplit` parts
-// of `split_pages` pages; each part's sums go to part_o [nsplit, T, H, d] (float32)
-// and, where weights are taken, each head's to part_w [planes, B, lcap], one plane
-// per (query tile, head); a second kernel joins them in a fixed order.
-constexpr int kCacheRows = 16;  // query rows up to which the few-rows kernel runs (bf16)
+// 8-bit cache: attention over the cache.  Three kernels: float32 on CUDA cores, bf16
+// of up to kCacheRows query rows a sequence, bf16 of more (tensor cores).  The first
+// two cut the key axis into `nsplit` parts of `split_pages` pages, whose sums go to
+// part_o [nsplit, T, H, d] (float32); the third cuts all its tiles into `ctas` runs,
+// with two slots [128, d] of part_o and two piece records each.  Where weights are
+// taken, each (query tile, head)'s go to a plane of part_w [planes, B, lcap].  A second
+// kernel joins them in a fixed order.
+constexpr int kCacheRows = 16;
+enum CacheKernel { CACHE_F32, CACHE_ROWS, CACHE_TC };
 struct CacheAttnPlan {
-    bool rows;  // the few-rows kernel
+    CacheKernel kernel;
     int nsplit, split_pages;
-    int tile_rows;
-    int qtiles;  // query tiles that have planes of their own
+    int ctas;
+    int tile_rows, qtiles;  // query rows of a tile, tiles of a sequence
     int64_t lcap;
-    size_t part_o_bytes, part_w_bytes;
+    size_t part_o_bytes, part_w_bytes, piece_bytes;
+};
+struct CacheAttnPiece {
+    int64_t row;  // first row of the unit's queries
+    int head, cols, last;
 };
 struct CacheAttnArgs {
     CacheCall c;
@@ -201,10 +209,12 @@ struct CacheAttnArgs {
     void *out;
     float *weights_out;
     float *part_o, *part_w;
+    CacheAttnPiece *pieces;
 };
-cudaError_t launch_cache_attn_rows(const CacheAttnArgs &a, cudaStream_t stream);
 CacheAttnPlan cache_attn_plan(const CacheCall &c, bool bf16, bool with_weights);
-bool cache_attn_grid_ok(const CacheAttnArgs &a);  // its launches stay below the grid limit
+bool cache_attn_fits(const CacheAttnArgs &a);  // its launches and coordinates stay below their limits
 cudaError_t launch_cache_attn(const CacheAttnArgs &a, bool bf16, cudaStream_t stream);
+cudaError_t launch_cache_attn_rows(const CacheAttnArgs &a, cudaStream_t stream);
+cudaError_t launch_cache_attn_tc(const CacheAttnArgs &a, cudaStream_t stream);
 
 }  // namespace hstu

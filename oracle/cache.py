@@ -101,8 +101,9 @@ def append(pool, k, v, table, lens, seq_pos, offsets, ts, num_targets):
 def attn(pool, q, table, lens, seq_pos, offsets, ts, num_targets, rab_pos, rab_time, inv_n, pos_lo, pos_hi,
          own=False, addend=None):
     """(out [T, H, d], weights [N, 64], terms): terms has what error bounds are made of,
-    per output the root of sum (P v)^2, sum (h v)^2 and sum (m v)^2 over the cached tokens,
-    where h = |s| / 2, m = sum |q k| + |bias|; per cached token the same of P, h and m."""
+    per output the roots of the sums over the cached tokens of (P v)^2, (h v)^2, (m v)^2 and
+    (x v)^2, where h = |s| / 2, m = sum |q k| + |bias|, x = max |q| sum |k|, all times
+    inv_n; per cached token the same without v."""
     T, H, d = q.shape
     pos = lens if seq_pos is None else seq_pos
     rab_pos = np.broadcast_to(rab_pos.astype(np.float64), (H, rab_pos.shape[-1]))
@@ -110,8 +111,8 @@ def attn(pool, q, table, lens, seq_pos, offsets, ts, num_targets, rab_pos, rab_t
     nb = rab_time.shape[1]
     out = np.zeros((T, H, d)) if addend is None else addend.astype(np.float64).copy()
     w = pool["weights"].astype(np.float64).copy()
-    t_out = {x: np.zeros((T, H, d)) for x in "Phm"}
-    t_w = {x: np.zeros(w.shape) for x in "Phm"}
+    t_out = {x: np.zeros((T, H, d)) for x in "Phmx"}
+    t_w = {x: np.zeros(w.shape) for x in "Phmx"}
     for b in range(len(lens)):
         s0, n, L = int(offsets[b]), int(offsets[b + 1] - offsets[b]), int(lens[b])
         if n == 0 or L == 0:
@@ -131,10 +132,11 @@ def attn(pool, q, table, lens, seq_pos, offsets, ts, num_targets, rab_pos, rab_t
             bias = rab_pos[h][dp] + rab_time[h][bucket]
             s = qq @ kk.T + bias
             m = np.abs(qq) @ np.abs(kk).T + np.abs(rab_pos[h][dp]) + np.abs(rab_time[h][bucket])
+            big = np.abs(qq).max(1)[:, None] * np.abs(kk).sum(1)[None, :]
             P = s / (1.0 + np.exp(-s)) * inv_n
             out[s0:s0 + n, h] += P @ vv
             w[page, slot] += np.abs(P).sum(0)
-            for x, a in (("P", P), ("h", 0.5 * np.abs(s) * inv_n), ("m", m * inv_n)):
+            for x, a in (("P", P), ("h", 0.5 * np.abs(s) * inv_n), ("m", m * inv_n), ("x", big * inv_n)):
                 t_out[x][s0:s0 + n, h] = np.sqrt((a * a) @ (vv * vv))
                 t_w[x][page, slot] += (a * a).sum(0)
     return out, w, dict(out=t_out, w={x: np.sqrt(a) for x, a in t_w.items()})

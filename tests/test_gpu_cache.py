@@ -6,8 +6,10 @@ Bounds of the attention.  With u = 2^-24, a score s = q.k + bias of m = sum |q k
 carries at most c_m m, P = SiLU(s) / N at most c_P P, and the tanh form c_h h, h = |s| / 2N:
   float32: c_m = 1.1 (d + 8) u (d products and sums; |SiLU'| <= 1.1), c_P = 2^-22 (expf to
            2 u, a division, two products);
-  bf16:    c_m = 1.1 (2^-17 + (d + 8) u), a query element being held to 2^-18 of its row's
-           largest; c_P = 2^-8 (P to 16 bits); c_h = 2^-10 (tanh.approx: 2^-11 of tanh).
+  bf16:    c_m as float32; c_x = 1.1 2^-14 on x = max |q| sum |k|: two E4M3 parts hold a
+           query element to 2^-10 of a scale whose rows' largest magnitude is above 224,
+           that is 2^-17.8 of it, and a row's own largest is at least 2^-3 of that;
+           c_P = 2^-8 (P to 16 bits); c_h = 2^-10 (tanh.approx: 2^-11 of tanh).
 The errors of the cached tokens' terms are independent, so a sum of them stays within six
 times the root of the sum of their squares; float32 sums add L u, the output's own rounding
 half a step.  A token's weight sums n H terms of one sign: there the h term counts fully."""
@@ -198,12 +200,12 @@ def _want_attn(x, own=False, add=True):
 def _check_attn(x, out, want, terms, wout=None, want_w=None, base=None):
     bf16 = x["q"].dtype == torch.bfloat16
     H, d = x["q"].shape[1:]
-    c_m = 1.1 * ((2.0 ** -17 if bf16 else 0.0) + (d + 8) * U)
+    c_m, c_x = 1.1 * (d + 8) * U, 1.1 * 2.0 ** -14 if bf16 else 0.0
     c_P, c_h = (2.0 ** -8, 2.0 ** -10) if bf16 else (2.0 ** -22, 0.0)
     L = x["max_len"]
     t = terms["out"]
     half = torch.finfo(x["q"].dtype).eps / 2
-    tol = 6 * ((c_P + L * U) * t["P"] + c_h * t["h"] + c_m * t["m"]) * (1 + half) + half * np.abs(want) + 1e-30
+    tol = 6 * ((c_P + L * U) * t["P"] + c_h * t["h"] + c_m * t["m"] + c_x * t["x"]) * (1 + half) + half * np.abs(want) + 1e-30
     err = np.abs(_values(out) - want)
     assert np.all(err <= tol), f"output off by {np.max(err / tol):.2f} of its bound"
     if wout is None:
@@ -216,7 +218,7 @@ def _check_attn(x, out, want, terms, wout=None, want_w=None, base=None):
     w = terms["w"]
     n = x["max_new"] * H
     c_Pw = 2.0 ** -8 if bf16 else 2.0 ** -22
-    tol = 6 * (c_Pw + n * U) * w["P"] + np.sqrt(n) * c_h * w["h"] + 6 * c_m * w["m"] + 2 * U * np.abs(want_w)
+    tol = 6 * (c_Pw + n * U) * w["P"] + np.sqrt(n) * c_h * w["h"] + 6 * (c_m * w["m"] + c_x * w["x"]) + 2 * U * np.abs(want_w)
     err = np.abs(got - want_w)[mine]
     assert np.all(err <= tol[mine] + 1e-30), f"weights off by {np.max(err / (tol[mine] + 1e-30)):.2f} of their bound"
     np.testing.assert_array_equal(got[~mine], base[~mine])
@@ -305,7 +307,7 @@ def test_attention_drops_and_flags(new, cuda_device):
     assert ops.hstu_check_device_flag(ws) == (5, 64)
     want, _, terms = _want_attn(x)
     rows = np.r_[0:new, 2 * new:3 * new]
-    sub = {n: t[rows] for n, t in terms["out"].items()}
+    sub = {n: a[rows] for n, a in terms["out"].items()}
     _check_attn(x, out[torch.as_tensor(rows, device=cuda_device)], want[rows], {"out": sub})
     assert torch.equal(out[new:2 * new], fill[new:2 * new])
     bad = dict(x, table=x["table"].copy())
