@@ -213,7 +213,7 @@ bool cache_attn_fits(const CacheAttnArgs &a)
     const double limit = 2147483647.0;
     const double w_blocks = (double)(a.plan.lcap / 256 + 1) * c.B;
     if (a.plan.kernel == CACHE_TC)  // TMA coordinates: rows of the pool's codes
-        return (double)c.num_pages * c.H * kPage < limit && w_blocks + c.B + 4.0 * a.plan.ctas < limit;
+        return (double)c.num_pages * c.H * std::max(kPage, c.d) < limit && w_blocks + c.B + 16.0 * a.plan.ctas < limit;
     return (double)c.B * a.plan.qtiles * c.H * a.plan.nsplit < limit &&
            ((double)c.max_seq_len * c.H * c.d / 1024 + 2) * c.B + w_blocks < limit;
 }
