@@ -71,7 +71,7 @@ __device__ __forceinline__ void cache_join_weight(const CacheAttnArgs &a, int b,
     const int page = table_page(c.table, c, b, j / kPage);
     if (page < 0)
         return;
-    const int planes = (s.n + a.plan.tile_rows - 1) / a.plan.tile_rows * c.H;
+    const int planes = (s.n + a.plan.plane_rows - 1) / a.plan.plane_rows * c.H;
     float sum = 0.f;
     for (int p = 0; p < planes; p++)
         sum += a.part_w[((int64_t)p * c.B + b) * a.plan.lcap + j];

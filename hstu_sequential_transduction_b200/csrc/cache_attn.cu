@@ -187,8 +187,10 @@ CacheAttnPlan cache_attn_plan(const CacheCall &c, bool bf16, bool with_weights)
     const int64_t pages = (c.max_cache_len + kPage - 1) / kPage;
     const int64_t sms = device_info().sms;
     p.kernel = !bf16 ? CACHE_F32 : c.max_seq_len <= kCacheRows ? CACHE_ROWS : CACHE_TC;
-    p.tile_rows = p.kernel == CACHE_TC ? kTcTile : kRows;
-    p.qtiles = (c.max_seq_len + p.tile_rows - 1) / p.tile_rows;
+    const int tile_rows = p.kernel == CACHE_TC ? kTcTile : kRows;
+    p.qtiles = (c.max_seq_len + tile_rows - 1) / tile_rows;
+    p.plane_rows = p.kernel == CACHE_TC ? 64 : kRows;
+    const int64_t planes = (int64_t)(c.max_seq_len + p.plane_rows - 1) / p.plane_rows * c.H;
     p.lcap = pages * kPage;
     const int64_t units = (int64_t)c.B * c.H * p.qtiles;
     if (units > 0 && pages > 0 && p.kernel == CACHE_TC) {
@@ -203,7 +205,7 @@ CacheAttnPlan cache_attn_plan(const CacheCall &c, bool bf16, bool with_weights)
         p.nsplit = (int)((pages + p.split_pages - 1) / p.split_pages);
         p.part_o_bytes = align256(sizeof(float) * (size_t)p.nsplit * c.T * c.H * c.d);
     }
-    p.part_w_bytes = with_weights ? align256(sizeof(float) * (size_t)p.qtiles * c.H * c.B * p.lcap) : 0;
+    p.part_w_bytes = with_weights ? align256(sizeof(float) * (size_t)planes * c.B * p.lcap) : 0;
     return p;
 }
 

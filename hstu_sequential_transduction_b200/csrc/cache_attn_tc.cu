@@ -52,7 +52,7 @@ constexpr int kCutTiles = 8;  // what a cut unit costs (its pieces' traffic and 
 constexpr int kPanel = 16384; // 64 query columns of P^T: 128 keys x 128 bytes
 
 enum Bars { K_FULL = 0, K_EMPTY = K_FULL + kKStages, C_FULL = K_EMPTY + kKStages, C_EMPTY = C_FULL + kVStages,
-            S_FULL = C_EMPTY + kVStages, P_FULL = S_FULL + 2, P_EMPTY = P_FULL + 2, V_FULL = P_EMPTY + 2,
+            S_FULL = C_EMPTY + kVStages, P_FULL = S_FULL + 4, P_EMPTY = P_FULL + 4, V_FULL = P_EMPTY + 4,
             V_EMPTY = V_FULL + 2, Q_FULL = V_EMPTY + 2, Q_EMPTY = Q_FULL + 2, O_FULL = Q_EMPTY + 2,
             O_FREE = O_FULL + 1, NBARS = O_FREE + 1 };
 
@@ -184,10 +184,19 @@ __device__ bool find_run(const CacheCall &c, int cta, int ctas, int64_t *sums, i
         hi = max(hi, (int)sums[2 * kW + w]);
     }
     // equal units: whole ones, unless that makes the longest run much longer than the mean
-    int64_t grain = 1;
-    if (lo == hi && (total / hi + ctas - 1) / ctas * hi <= total / ctas + kCutTiles)
-        grain = hi;
-    const int64_t start = total / grain * cta / ctas * grain, end = total / grain * (cta + 1) / ctas * grain;
+    int64_t start, end;
+    if (total <= 0xffffffffu / (unsigned)(ctas + kCutTiles + 1)) {  // a 64-bit division takes hundreds of cycles
+        const unsigned all = (unsigned)total, n = (unsigned)ctas;
+        unsigned grain = 1;
+        if (lo == hi && (all / hi + n - 1) / n * hi <= all / n + kCutTiles)
+            grain = hi;
+        const unsigned units = all / grain;
+        start = units * (unsigned)cta / n * grain;
+        end = units * (unsigned)(cta + 1) / n * grain;
+    } else {
+        start = total / ctas * cta + total % ctas * cta / ctas;
+        end = total / ctas * (cta + 1) + total % ctas * (cta + 1) / ctas;
+    }
     int64_t at = before + inc - mine;
     if (start < end && start >= at && start < at + mine) {
         for (int b = b0; b < b1; b++) {
@@ -218,34 +227,6 @@ __device__ __forceinline__ uint32_t odd_codes(uint32_t w) { return (w & 0x800080
 // Row of P^T of key r: the order in which the words above hold four keys.
 __device__ __forceinline__ int key_row(int r) { return (r & ~3) | ((r & 1) << 1) | ((r >> 1) & 1); }
 
-__device__ __forceinline__ uint64_t pack2(float x, float y)
-{
-    uint64_t d;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(x), "f"(y));
-    return d;
-}
-
-__device__ __forceinline__ float2 unpack2(uint64_t d)
-{
-    float2 f;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(d));
-    return f;
-}
-
-__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z)
-{
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(x), "l"(y), "l"(z));
-    return d;
-}
-
-// SiLU(2 h) of two values
-__device__ __forceinline__ float2 silu2(uint64_t h)
-{
-    const float2 f = unpack2(h);
-    return unpack2(fma2(h, pack2(tanh_approx(f.x), tanh_approx(f.y)), h));
-}
-
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
 {
     uint32_t d;
@@ -259,6 +240,47 @@ __device__ __forceinline__ uint32_t pow2_bf16x2(int e)  // two copies of 2^e, -1
     return x | (x << 16);
 }
 
+// SiLU(2 h)
+__device__ __forceinline__ float silu_half(float h) { return fmaf(h, tanh_approx(h), h); }
+
+// mbar_wait, but asleep until the phase ends (the hint: 1 ms at most) instead of
+// polling: ten waiting warps would take a third of the issue slots.
+__device__ __forceinline__ bool sleep_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag, WsHeader *hdr)
+{
+    auto try_wait = [&] {
+        uint32_t done;
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(done)
+            : "r"(bar), "r"(parity), "r"(1000000u)
+            : "memory");
+        return done != 0;
+    };
+    if (try_wait())
+        return true;
+    const long long t0 = clock64();
+    while (!try_wait()) {
+        if (*abort_flag)
+            return false;
+        if (clock64() - t0 > kWaitLimitCycles) {
+            *abort_flag = 1;
+            atomicOr(&hdr->flag, FLAG_TIMEOUT);
+            return false;
+        }
+    }
+    return true;
+}
+
+// One lane of a converged warp.  Under this predicate the compiler knows that one thread
+// issues; under `lane == 0` it wraps every TMA, MMA and commit in a loop over the active
+// lanes, which took 100 cycles an MMA.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p != 0;
+}
+
 // 32 lanes x 8 consecutive 32-bit columns
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float *v)
 {
@@ -268,24 +290,18 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float *v)
                  : "r"(taddr));
 }
 
-// P^T of eight scores (zeros for a dead key) into 16 bytes of a row of the panel.
-__device__ __forceinline__ void put_p8(const float *x, bool dead, bool live, unsigned char *dst)
+// P^T of eight scores into 16 bytes of a row of the panel.
+__device__ __forceinline__ void put_p8(const float *x, unsigned char *dst)
 {
-    uint32_t pk[4];
-#pragma unroll
-    for (int e = 0; e < 4; e++) {
-        pk[e] = pack_bf16(x[2 * e], x[2 * e + 1]);
-        if (dead)
-            pk[e] = live ? pk[e] : 0u;
-    }
-    *reinterpret_cast<uint4 *>(dst) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+    *reinterpret_cast<uint4 *>(dst) =
+        make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
 }
 
 // A chunk of 32 queries whose biases or scales differ: this key's P^T, and the sum of
 // its magnitudes over the first n.  Where the whole warp's pairs share an index of a
 // table, it is read once.  Eight queries at a time: the common loop keeps its registers.
 __device__ __forceinline__ float chunk_general(uint32_t taddr, int cc, int n, const CacheAttnArgs &a, const float *rp,
-                                               const float *rt, const QueryInfo &qi, bool dead, bool live, int pj,
+                                               const float *rt, const QueryInfo &qi, bool live, int pj,
                                                int64_t tj, float half_scale, unsigned char *dst, int row_p)
 {
     const int ch = cc >> 5;
@@ -318,11 +334,10 @@ __device__ __forceinline__ float chunk_general(uint32_t taddr, int cc, int n, co
         tmem_wait_ld();
 #pragma unroll
         for (int e = 0; e < 8; e++) {
-            const float hh = fmaf(x[e], half_scale * qi.scale[cc + e8 + e], 0.5f * b[e]);
-            x[e] = fmaf(hh, tanh_approx(hh), hh);
+            x[e] = silu_half(fmaf(x[e], half_scale * qi.scale[cc + e8 + e], 0.5f * b[e]));
             w += e8 + e < n ? fabsf(x[e]) : 0.f;
         }
-        put_p8(x, dead, live, dst + ((((cc + e8) >> 3 & 7) ^ (row_p & 7)) * 16));
+        put_p8(x, dst + ((((cc + e8) >> 3 & 7) ^ (row_p & 7)) * 16));
     }
     return w;
 }
@@ -361,7 +376,7 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
     if (threadIdx.x == 0) {
         for (int i = 0; i < NBARS; i++) {
             int n = 1;
-            if (i == P_FULL || i == P_FULL + 1 || i == Q_FULL || i == Q_FULL + 1)
+            if ((i >= P_FULL && i < P_FULL + 4) || i == Q_FULL || i == Q_FULL + 1)
                 n = 4;
             else if (i == V_FULL || i == V_FULL + 1 || (i >= C_EMPTY && i < C_EMPTY + kVStages))
                 n = D / 32;
@@ -383,7 +398,10 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(sm + LY::MISC);
     bool ok = true;
-    auto wait = [&](int i, int parity) { return mbar_wait(bar(i), parity & 1, abort_flag, hdr); };
+    auto wait = [&](int i, int parity) { return sleep_wait(bar(i), parity & 1, abort_flag, hdr); };
+
+    // by a whole warp that stays converged
+    auto wait_all = [&](int i, int parity) { return __all_sync(0xffffffffu, wait(i, parity)) != 0; };
 
     if (warp == 0) {
         // ---------------- codes ----------------
@@ -404,10 +422,10 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
                 const int page[2] = {__shfl_sync(0xffffffffu, held, 2 * (t % 16)),
                                      __shfl_sync(0xffffffffu, held, 2 * (t % 16) + 1)};
                 const uint32_t bytes = ((page[0] >= 0) + (page[1] >= 0)) * kPage * D;
-                ok = __all_sync(0xffffffffu, g < kKStages || wait(K_EMPTY + kst, g / kKStages - 1));
+                ok = g < kKStages || wait_all(K_EMPTY + kst, g / kKStages - 1);
                 if (!ok)
                     break;
-                if (lane == 0) {
+                if (elect_one()) {
                     mbar_expect_tx(bar(K_FULL + kst), bytes);
 #pragma unroll
                     for (int e = 0; e < 2; e++)
@@ -415,10 +433,10 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
                             tma_load_2d(base + LY::K + kst * LY::KT + e * kPage * D, &tk, 0,
                                         (page[e] * c.H + h) * kPage, bar(K_FULL + kst));
                 }
-                ok = __all_sync(0xffffffffu, g < kVStages || wait(C_EMPTY + vst, g / kVStages - 1));
+                ok = g < kVStages || wait_all(C_EMPTY + vst, g / kVStages - 1);
                 if (!ok)
                     break;
-                if (lane == 0) {
+                if (elect_one()) {
                     mbar_expect_tx(bar(C_FULL + vst), bytes);
 #pragma unroll
                     for (int e = 0; e < 2; e++)
@@ -430,64 +448,77 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
             }
         }
     } else if (warp == 1) {
-        // ---------------- MMAs ----------------
-        if (lane == 0) {
-            int issued = 0, done = 0, t = 0, piece = 0;
-            Walk w = start;
-            int count = w.count(), n = w.cols() > 64 ? 128 : 64;
-            uint32_t ring = 0;  // of the two tiles in flight: first, last, 128 columns; tile g in bits 4 (g & 1)
-            while (ok) {
-                if (w.left > 0 && issued < done + 2) {
-                    const int st = issued % kKStages, sb = issued & 1, qs = w.piece & 1;
-                    const bool first = t == 0, last = t + 1 == count;
-                    ok = (!first || wait(Q_FULL + qs, w.piece >> 1)) && wait(K_FULL + st, issued / kKStages);
+        // ---------------- S^T = K Q^T ----------------
+        int g = 0, it = 0;
+        for (Walk w = start; ok && w.left > 0; w.next(c)) {
+            const int qs = w.piece & 1, count = w.count(), halves = w.cols() > 64 ? 2 : 1;
+            if (!(ok = wait_all(Q_FULL + qs, w.piece >> 1)))
+                break;
+            for (int t = 0; ok && t < count; t++, g++) {
+                const int st = g % kKStages;
+                if (!(ok = wait_all(K_FULL + st, g / kKStages)))
+                    break;
+                // both halves at once where their buffers are neighbours
+                const int wide = halves == 2 && (it & 1) == 0 ? 2 : 1;
+                for (int hf = 0; hf < halves; hf += wide, it += wide) {
+                    // a buffer is free once the item four back has become P^T
+                    ok = (it < 4 || wait_all(P_FULL + (it & 3), (it >> 2) - 1)) &&
+                         (wide == 1 || it < 4 || wait_all(P_FULL + (it & 3) + 1, (it >> 2) - 1));
                     if (!ok)
                         break;
                     tc_fence_after();
-                    const uint32_t id = idesc_e4m3(128, 0, 0, 0) | ((uint32_t)(n >> 3) << 17);
-                    const uint64_t kd = code_desc<D>(base + LY::K + st * LY::KT);
-                    const uint64_t qd = code_desc<D>(base + LY::Q + 2 * qs * LY::KT);
+                    if (elect_one()) {
+                        const uint32_t id = idesc_e4m3(128, 0, 0, 0) | ((uint32_t)(64 * wide >> 3) << 17);
+                        const uint64_t kd = code_desc<D>(base + LY::K + st * LY::KT);
+                        const uint64_t qd = code_desc<D>(base + LY::Q + 2 * qs * LY::KT + hf * 64 * D);
 #pragma unroll
-                    for (int i = 0; i < 2 * (D / 32); i++)  // 32 bytes of a row a step: 2 in the address field
-                        umma_e4m3(tmem + sb * kTile, kd + 2 * (i % (D / 32)),
-                                  qd + i / (D / 32) * (LY::KT >> 4) + 2 * (i % (D / 32)), id, i > 0);
-                    umma_commit(bar(K_EMPTY + st));
-                    umma_commit(bar(S_FULL + sb));
-                    if (last)
-                        umma_commit(bar(Q_EMPTY + qs));
-                    ring = (ring & ~(15u << (4 * sb))) | ((first | last << 1 | (n == 128) << 2) << (4 * sb));
-                    issued++;
-                    t++;
-                    if (last) {
-                        w.next(c);
-                        t = 0;
-                        count = w.count();
-                        n = w.cols() > 64 ? 128 : 64;
+                        for (int i = 0; i < 2 * (D / 32); i++)  // 32 bytes of a row a step: 2 in the address field
+                            umma_e4m3(tmem + (it & 3) * 64, kd + 2 * (i % (D / 32)),
+                                      qd + i / (D / 32) * (LY::KT >> 4) + 2 * (i % (D / 32)), id, i > 0);
+                        umma_commit(bar(S_FULL + (it & 3)));
+                        if (wide == 2)
+                            umma_commit(bar(S_FULL + (it & 3) + 1));
+                        if (hf + wide == halves) {
+                            umma_commit(bar(K_EMPTY + st));
+                            if (t + 1 == count)
+                                umma_commit(bar(Q_EMPTY + qs));
+                        }
                     }
-                    continue;
+                    __syncwarp();
                 }
-                if (done == issued)
+            }
+        }
+    } else if (warp == 2) {
+        // ---------------- O^T += V^T P^T ----------------
+        int g = 0, it = 0;
+        for (Walk w = start; ok && w.left > 0; w.next(c)) {
+            const int count = w.count(), halves = w.cols() > 64 ? 2 : 1;
+            if (w.piece > 0 && !(ok = wait_all(O_FREE, w.piece - 1)))
+                break;
+            for (int t = 0; ok && t < count; t++, g++) {
+                const int vb = g & 1;
+                if (!(ok = wait_all(V_FULL + vb, g >> 1)))
                     break;
-                const int sb = done & 1;
-                const uint32_t r = ring >> (4 * sb);
-                ok = wait(P_FULL + sb, done >> 1) && wait(V_FULL + sb, done >> 1) &&
-                     (!(r & 1) || piece == 0 || wait(O_FREE, piece - 1));
-                if (!ok)
-                    break;
-                tc_fence_after();
-                const uint32_t id = idesc_bf16(128, 0, 0, 1) | ((uint32_t)((r & 4 ? 128 : 64) >> 3) << 17);
-                const uint64_t pd = smem_desc_sw128(base + LY::P + sb * 2 * kPanel, kPanel, 1024);
+                for (int hf = 0; hf < halves; hf++, it++) {
+                    if (!(ok = wait_all(P_FULL + (it & 3), it >> 2)))
+                        break;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        constexpr uint32_t id = idesc_bf16(128, 64, 0, 1);
+                        const uint64_t pd = smem_desc_sw128(base + LY::P + (it & 3) * kPanel, kPanel, 1024);
 #pragma unroll
-                for (int ks = 0; ks < kTile / 16; ks++)  // 16 rows of P^T a step
-                    umma_bf16_ts(tmem + 256, tmem + 384 + sb * 64 + ks * 8, pd + ks * (2048 >> 4), id,
-                                 !(r & 1) || ks > 0);
-                umma_commit(bar(V_EMPTY + sb));
-                umma_commit(bar(P_EMPTY + sb));
-                if (r & 2) {
-                    umma_commit(bar(O_FULL));
-                    piece++;
+                        for (int ks = 0; ks < kTile / 16; ks++)  // 16 rows of P^T a step
+                            umma_bf16_ts(tmem + 256 + hf * 64, tmem + 384 + vb * 64 + ks * 8, pd + ks * (2048 >> 4), id,
+                                         ks > 0 || t > 0);
+                        umma_commit(bar(P_EMPTY + (it & 3)));
+                        if (hf + 1 == halves) {
+                            umma_commit(bar(V_EMPTY + vb));
+                            if (t + 1 == count)
+                                umma_commit(bar(O_FULL));
+                        }
+                    }
+                    __syncwarp();
                 }
-                done++;
             }
         }
     } else if (warp >= 12) {
@@ -501,74 +532,96 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
                 break;
             {
                 QueryInfo &qi = info[qs];
-                const bool have = row < cols;
+                // LR lanes a row, eight elements a lane.  The row passes through the places of
+                // its two parts (eight bytes a lane in each), read back by the lane that wrote.
+                constexpr int LR = D / 8, RI = 32 / LR;
+                const int chunk = row >> 5, lr = lane / LR, lc = lane % LR;
                 const __nv_bfloat16 *qp =
-                    static_cast<const __nv_bfloat16 *>(a.q) + (w.s.s0 + q0 + (have ? row : 0)) * a.ldq + (int64_t)h * D;
-                uint32_t m = 0;  // largest magnitude as bf16 bits
-                auto load8 = [&](int e) {
-                    return have ? *reinterpret_cast<const uint4 *>(qp + 8 * e) : make_uint4(0u, 0u, 0u, 0u);
-                };
-#pragma unroll
-                for (int e = 0; e < D / 8; e++) {
-                    const uint4 x = load8(e);
-                    const uint32_t ww[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                    for (int i = 0; i < 4; i++)
-                        m = max(m, max((ww[i] & 0x7fffu) << 16, ww[i] & 0x7fff0000u));
-                }
-                const uint32_t all = __reduce_max_sync(0xffffffffu, m);
-                // one scale for the warp's rows if none lies far below
-                const bool far = m != 0 && (int)(all >> 23) - (int)(m >> 23) > 2;
-                const bool one = !__any_sync(0xffffffffu, far);
-                const float scale = block_scale(one ? all : m), inv = scale_inverse(scale);
-                const int i0 = q0, i = q0 + (have ? row : 0);
+                    static_cast<const __nv_bfloat16 *>(a.q) + (w.s.s0 + q0) * a.ldq + (int64_t)h * D + 8 * lc;
+                unsigned char *q1 = sm + LY::Q + 2 * qs * LY::KT;
+                auto place = [&](int rr) { return q1 + rr * D + code_chunk<D>(rr, lc >> 1) * 16 + 8 * (lc & 1); };
+                // positions and stamps of the chunk: their range
+                const int i = q0 + (row < cols ? row : 0);
                 const int pi = w.s.pos + token_pos(i, w.s.hist, a.cand_own);
                 const int64_t ti = c.ts[w.s.s0 + i];
-                const bool same = pi == w.s.pos + token_pos(i0, w.s.hist, a.cand_own) && ti == c.ts[w.s.s0 + i0];
-                const bool all_same = __all_sync(0xffffffffu, same);
-                // positions and stamps of the chunk: their range
+                const bool all_same = __all_sync(0xffffffffu, pi == w.s.pos + token_pos(q0, w.s.hist, a.cand_own) &&
+                                                                  ti == c.ts[w.s.s0 + q0]);
                 int plo = pi, phi = pi;
                 int64_t tlo = ti, thi = ti;
+                if (!all_same) {
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) {
-                    plo = min(plo, __shfl_xor_sync(0xffffffffu, plo, o));
-                    phi = max(phi, __shfl_xor_sync(0xffffffffu, phi, o));
-                    tlo = min(tlo, __shfl_xor_sync(0xffffffffu, tlo, o));
-                    thi = max(thi, __shfl_xor_sync(0xffffffffu, thi, o));
+                    for (int o = 16; o > 0; o >>= 1) {
+                        plo = min(plo, __shfl_xor_sync(0xffffffffu, plo, o));
+                        phi = max(phi, __shfl_xor_sync(0xffffffffu, phi, o));
+                        tlo = min(tlo, __shfl_xor_sync(0xffffffffu, tlo, o));
+                        thi = max(thi, __shfl_xor_sync(0xffffffffu, thi, o));
+                    }
                 }
-                qi.scale[row] = scale;
+                // largest magnitude of each row, as bf16 bits at a float's place
+                auto row_max = [&](const uint32_t *ww) {
+                    uint32_t m = 0;
+#pragma unroll
+                    for (int e = 0; e < 4; e++)
+                        m = max(m, max((ww[e] & 0x7fffu) << 16, ww[e] & 0x7fff0000u));
+#pragma unroll
+                    for (int o = LR / 2; o > 0; o >>= 1)
+                        m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+                    return m;
+                };
+                uint32_t all = 0, least = 0xffffffffu;
+                {
+                    uint4 x[LR];
+#pragma unroll
+                    for (int j = 0; j < LR; j++) {
+                        const int rr = 32 * chunk + RI * j + lr;
+                        x[j] = rr < cols ? *reinterpret_cast<const uint4 *>(qp + rr * a.ldq) : make_uint4(0u, 0u, 0u, 0u);
+                    }
+#pragma unroll
+                    for (int j = 0; j < LR; j++) {
+                        const uint32_t ww[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+                        const uint32_t m = row_max(ww);
+                        all = max(all, m);
+                        least = min(least, m ? m : 0xffffffffu);
+                        unsigned char *at = place(32 * chunk + RI * j + lr);
+                        *reinterpret_cast<uint2 *>(at) = make_uint2(ww[0], ww[1]);
+                        *reinterpret_cast<uint2 *>(at + LY::KT) = make_uint2(ww[2], ww[3]);
+                    }
+                }
+                all = __reduce_max_sync(0xffffffffu, all);
+                least = __reduce_min_sync(0xffffffffu, least);
+                // one scale for the chunk's rows if none lies far below
+                const bool one = all == 0 || (all >> 23) - (least >> 23) <= 2;
                 qi.pos[row] = pi;
                 qi.ts[row] = ti;
                 if (lane == 0) {
-                    qi.chunk_scale[row >> 5] = one ? scale : -1.f;
-                    qi.chunk_same[row >> 5] = all_same;
-                    qi.pos_lo[row >> 5] = plo;
-                    qi.pos_hi[row >> 5] = phi;
-                    qi.ts_lo[row >> 5] = tlo;
-                    qi.ts_hi[row >> 5] = thi;
+                    qi.chunk_scale[chunk] = one ? block_scale(all) : -1.f;
+                    qi.chunk_same[chunk] = all_same;
+                    qi.pos_lo[chunk] = plo;
+                    qi.pos_hi[chunk] = phi;
+                    qi.ts_lo[chunk] = tlo;
+                    qi.ts_hi[chunk] = thi;
                 }
-                unsigned char *q1 = sm + LY::Q + 2 * qs * LY::KT + row * D, *q2 = q1 + LY::KT;
-#pragma unroll 2
-                for (int e = 0; e < D / 16; e++) {  // read again: held, the row would not fit the registers
-                    const uint4 x0 = load8(2 * e), x1 = load8(2 * e + 1);
-                    const uint32_t ww[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-                    uint32_t hi[4], lo[4];
+#pragma unroll 4
+                for (int j = 0; j < LR; j++) {
+                    const int rr = 32 * chunk + RI * j + lr;
+                    unsigned char *at = place(rr);
+                    const uint2 x0 = *reinterpret_cast<const uint2 *>(at);
+                    const uint2 x1 = *reinterpret_cast<const uint2 *>(at + LY::KT);
+                    const uint32_t ww[4] = {x0.x, x0.y, x1.x, x1.y};
+                    const float scale = block_scale(one ? all : row_max(ww)), inv = scale_inverse(scale);
+                    if (lc == 0)
+                        qi.scale[rr] = scale;
+                    uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
 #pragma unroll
-                    for (int i4 = 0; i4 < 4; i4++) {
-                        hi[i4] = lo[i4] = 0;
-#pragma unroll
-                        for (int e2 = 0; e2 < 2; e2++) {
-                            const uint32_t y = ww[2 * i4 + e2];
-                            const float y0 = __uint_as_float(y << 16) * inv, y1 = __uint_as_float(y & 0xffff0000u) * inv;
-                            const uint32_t p = f32x2_to_e4m3x2(y0, y1);
-                            const float2 f = e4m3x2_to_f32x2(p);
-                            hi[i4] |= p << (16 * e2);
-                            lo[i4] |= f32x2_to_e4m3x2(y0 - f.x, y1 - f.y) << (16 * e2);
-                        }
+                    for (int e = 0; e < 4; e++) {
+                        const float y0 = __uint_as_float(ww[e] << 16) * inv, y1 = __uint_as_float(ww[e] & 0xffff0000u) * inv;
+                        const uint32_t p = f32x2_to_e4m3x2(y0, y1);
+                        const float2 f = e4m3x2_to_f32x2(p);
+                        hi[e >> 1] |= p << (16 * (e & 1));
+                        lo[e >> 1] |= f32x2_to_e4m3x2(y0 - f.x, y1 - f.y) << (16 * (e & 1));
                     }
-                    const int at = code_chunk<D>(row, e) * 16;
-                    *reinterpret_cast<uint4 *>(q1 + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4 *>(q2 + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    *reinterpret_cast<uint2 *>(at) = make_uint2(hi[0], hi[1]);
+                    *reinterpret_cast<uint2 *>(at + LY::KT) = make_uint2(lo[0], lo[1]);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -602,52 +655,46 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
                 if (!(ok = wait(C_FULL + vst, g / kVStages) && (g < 2 || wait(V_EMPTY + vb, (g >> 1) - 1))))
                     break;
                 tc_fence_after();
+                // 32 keys at a time, rolled: the roles' loops share the instruction cache
+                const unsigned char *vrow = sm + LY::V + vst * LY::KT + dim * kPage;
+                const uint32_t dst = tmem + ((uint32_t)(quarter * 32) << 16) + 384 + vb * 64;
+#pragma unroll 1
+                for (int q = 0; q < 4; q++) {
+                    const int e = q >> 1, n = w.s.len - k * kTile - 32 * q, bits = e ? sc[1] : sc[0];
+                    const unsigned char *src = vrow + e * kPage * D;
+                    uint32_t v[8];
 #pragma unroll
-                for (int e = 0; e < 2; e++) {
-                    uint4 v[4];
-                    const unsigned char *vrow = sm + LY::V + vst * LY::KT + e * kPage * D + dim * kPage;
-#pragma unroll
-                    for (int i = 0; i < 4; i++)
-                        v[i] = *reinterpret_cast<const uint4 *>(vrow + (i ^ ((dim >> 1) & 3)) * 16);
+                    for (int i = 0; i < 2; i++) {
+                        const uint4 y = *reinterpret_cast<const uint4 *>(src + ((2 * (q & 1) + i) ^ ((dim >> 1) & 3)) * 16);
+                        v[4 * i] = y.x, v[4 * i + 1] = y.y, v[4 * i + 2] = y.z, v[4 * i + 3] = y.w;
+                    }
                     // codes behind the last token, or of a page that was not loaded, may be anything
-                    const int n = w.s.len - (2 * k + e) * kPage;
-                    if (n < kPage || sc[e] == 0) {
+                    if (n < 32 || bits == 0) {
+                        const int keep = bits == 0 ? 0 : n;
 #pragma unroll
-                        for (int i = 0; i < 4; i++) {
-                            auto keep = [&](uint32_t x, int at) {
-                                return sc[e] == 0 || n <= at ? 0u : n >= at + 4 ? x : x & ((1u << (8 * (n - at))) - 1u);
-                            };
-                            v[i] = make_uint4(keep(v[i].x, 16 * i), keep(v[i].y, 16 * i + 4),
-                                              keep(v[i].z, 16 * i + 8), keep(v[i].w, 16 * i + 12));
-                        }
+                        for (int i = 0; i < 8; i++)
+                            v[i] = keep >= 4 * i + 4 ? v[i] : keep <= 4 * i ? 0u : v[i] & ((1u << (8 * (keep - 4 * i))) - 1u);
                     }
                     // times the scale 2^x and 2^120, in two factors where bf16 has no 2^(120 + x); a NaN scale as it is
-                    const int x = (sc[e] >> 23 & 255) - 127;
+                    const int x = (bits >> 23 & 255) - 127;
                     const bool nan = x == 128;
                     const int x1 = nan ? 120 : min(120 + max(x, -126), 127);
                     const uint32_t f1 = pow2_bf16x2(x1);
-                    const uint32_t f2 = nan ? 0x7fff7fffu : pow2_bf16x2(max(120 + x - x1, 0));
+                    uint32_t pk[16];
 #pragma unroll
-                    for (int hf = 0; hf < 2; hf++) {
-                        uint32_t pk[16];
-#pragma unroll
-                        for (int i = 0; i < 2; i++) {
-                            const uint4 q = v[2 * hf + i];
-                            const uint32_t ww[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-                            for (int j = 0; j < 4; j++) {
-                                pk[8 * i + 2 * j] = mul_bf16x2(even_codes(ww[j]), f1);
-                                pk[8 * i + 2 * j + 1] = mul_bf16x2(odd_codes(ww[j]), f1);
-                            }
-                        }
-                        if (nan || 120 + x > 127)
-#pragma unroll
-                            for (int i = 0; i < 16; i++)
-                                pk[i] = mul_bf16x2(pk[i], f2);
-                        tmem_st16(tmem + ((uint32_t)(quarter * 32) << 16) + 384 + vb * 64 + e * 32 + hf * 16, pk);
+                    for (int i = 0; i < 8; i++) {
+                        pk[2 * i] = mul_bf16x2(even_codes(v[i]), f1);
+                        pk[2 * i + 1] = mul_bf16x2(odd_codes(v[i]), f1);
                     }
-                    sc[e] = next[e];
+                    if (nan || 120 + x > 127) {
+                        const uint32_t f2 = nan ? 0x7fff7fffu : pow2_bf16x2(max(120 + x - x1, 0));
+#pragma unroll
+                        for (int i = 0; i < 16; i++)
+                            pk[i] = mul_bf16x2(pk[i], f2);
+                    }
+                    tmem_st16(dst + 16 * q, pk);
                 }
+                sc[0] = next[0], sc[1] = next[1];
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -662,15 +709,20 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
         const int group = (warp - 4) >> 2, quarter = warp & 3;
         const int r = quarter * 32 + lane, row_p = key_row(r);  // key of the tile, its row of P^T
         const uint32_t trow = tmem + ((uint32_t)(quarter * 32) << 16);
-        int g0 = 0;  // tiles before this piece
+        int it0 = 0;  // items before this piece
         for (Walk w = start; ok && w.left > 0; w.next(c)) {
             const int qs = w.piece & 1, h = w.head(), q0 = w.q0(), cols = w.cols(), count = w.count();
             const float *rp = a.rab_pos + h * a.pos_hstride, *rt = a.rab_time + h * a.time_hstride;
             const QueryInfo &qi = info[qs];
-            float *plane = a.part_w ? a.part_w + ((int64_t)((q0 / kTile) * c.H + h) * c.B + w.b) * a.plan.lcap : nullptr;
-            // The group's tiles of this piece are those with g % 2 = group.  What a tile needs
-            // of this thread's key is fetched ahead, one step of the chain a tile: the page, the
-            // token's position, stamp and scale, the bias of column 0.
+            // Items (a tile's 64 columns) alternate between the groups: of a tile with two,
+            // each group takes one; of tiles with one, every other tile.
+            const int halves = cols > 64 ? 2 : 1, step = halves == 2 ? 1 : 2;
+            const int first = halves == 2 ? 0 : (it0 ^ group) & 1, hf = halves == 2 ? (it0 ^ group) & 1 : 0;
+            const int c0 = hf * 64, n = min(cols - c0, 64);
+            float *plane =
+                a.part_w ? a.part_w + ((int64_t)((q0 + c0) / 64 * c.H + h) * c.B + w.b) * a.plan.lcap : nullptr;
+            // What a tile needs of this thread's key is fetched ahead, one step of the chain a
+            // tile: the page, the token's position, stamp and scale, the bias of column 0.
             struct Key {
                 bool live;
                 int pos;
@@ -691,20 +743,22 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
                 }
                 return y;
             };
-            const int first = (g0 & 1) == group ? 0 : 1;
-            Key key = key_at(page_at(first)), ahead = key_at(page_at(first + 2));
-            int page = page_at(first + 4);
+            Key key = key_at(page_at(first)), ahead = key_at(page_at(first + step));
+            int page = page_at(first + 2 * step);
             if (!(ok = wait(Q_FULL + qs, w.piece >> 1)))
                 break;
-            const int p_i = qi.pos[0];
+            const int p_i = qi.pos[0], ch = c0 >> 5, ch1 = n > 32 ? ch + 1 : ch;
             const int64_t t_i = qi.ts[0];
+            const float s0 = qi.chunk_scale[ch], s1 = qi.chunk_scale[ch1];
+            const bool same = qi.chunk_same[ch] && qi.chunk_same[ch1] && s0 != -1.f && s1 != -1.f &&
+                              (!plane || n % 32 == 0);
             float bp = 0.f, bt = 0.f;
             if (key.live) {
                 bp = rp[pos_index(p_i, key.pos, a.pos_lo, a.pos_hi)];
                 bt = rt[time_bucket(t_i, key.ts, a.nb)];
             }
-            for (int t = first; t < count; t += 2) {
-                const int g = g0 + t, k = w.k + t;
+            for (int t = first; t < count; t += step) {
+                const int it = it0 + (halves == 2 ? 2 * t + hf : t), k = w.k + t, b = it & 3;
                 const Key me = key;
                 const float bias = 0.5f * (bp + bt), half_scale = 0.5f * me.scale;
                 key = ahead;
@@ -714,100 +768,114 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
                     bt = rt[time_bucket(t_i, key.ts, a.nb)];
                 }
                 ahead = key_at(page);
-                page = page_at(t + 6);
-                if (!(ok = wait(S_FULL + group, g >> 1) && (g < 2 || wait(P_EMPTY + group, (g >> 1) - 1))))
+                page = page_at(t + 3 * step);
+                if (!(ok = wait(S_FULL + b, it >> 2) && (it < 4 || wait(P_EMPTY + b, (it >> 2) - 1))))
                     break;
                 tc_fence_after();
-                const bool dead = __any_sync(0xffffffffu, !me.live);
                 float wsum = 0.f;
-                unsigned char *prow = sm + LY::P + group * 2 * kPanel + row_p * 128;
+                unsigned char *prow = sm + LY::P + b * kPanel + row_p * 128;
+                const uint32_t taddr = trow + b * 64;
+                if (same) {
 #pragma unroll 1
-                for (int cc = 0; cc < cols; cc += 32) {
-                    unsigned char *dst = prow + (cc >> 6) * kPanel;
-                    const uint32_t taddr = trow + group * kTile + cc;
-                    const float cs = qi.chunk_scale[cc >> 5];
-                    if (!qi.chunk_same[cc >> 5] || cs == -1.f) {
-                        wsum += chunk_general(taddr, cc, cols - cc, a, rp, rt, qi, dead, me.live, me.pos, me.ts,
-                                              half_scale, dst, row_p);
-                        continue;
-                    }
-                    float x[32];
-                    tmem_ld32(taddr, x);
-                    tmem_wait_ld();
-                    const uint64_t b2 = pack2(bias, bias), f2 = pack2(half_scale * cs, half_scale * cs);
+                    for (int q = 0; 32 * q < n; q++) {
+                        float x[32];
+                        tmem_ld32(taddr + 32 * q, x);
+                        tmem_wait_ld();
+                        const float f = half_scale * (q ? s1 : s0);
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        const float2 y = silu2(fma2(pack2(x[e], x[e + 1]), f2, b2));
-                        x[e] = y.x, x[e + 1] = y.y;
-                    }
+                        for (int e = 0; e < 32; e++)
+                            x[e] = silu_half(fmaf(x[e], f, bias));
 #pragma unroll
-                    for (int e = 0; e < 4; e++)
-                        put_p8(x + 8 * e, dead, me.live, dst + ((((cc >> 3) & 4) + e) ^ (row_p & 7)) * 16);
-                    if (plane) {
-                        const int n = cols - cc;
-                        float w0 = 0.f, w1 = 0.f;
-                        if (n >= 32) {
+                        for (int e = 0; e < 4; e++)
+                            put_p8(x + 8 * e, prow + ((4 * q + e) ^ (row_p & 7)) * 16);
+                        if (plane) {
+                            float w0 = 0.f, w1 = 0.f;
 #pragma unroll
                             for (int e = 0; e < 32; e += 2)
                                 w0 += fabsf(x[e]), w1 += fabsf(x[e + 1]);
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 32; e++)
-                                w0 += e < n ? fabsf(x[e]) : 0.f;
+                            wsum += w0 + w1;
                         }
-                        wsum += w0 + w1;
                     }
+                } else {
+                    for (int cc = 0; cc < n; cc += 32)
+                        wsum += chunk_general(taddr + cc, c0 + cc, n - cc, a, rp, rt, qi, me.live, me.pos, me.ts,
+                                              half_scale, prow, row_p);
                 }
+                if (!me.live)  // no token, and S^T of whatever the tile holds there: P is 0
+                    for (int e = 0; e < 8; e++)
+                        *reinterpret_cast<uint4 *>(prow + e * 16) = make_uint4(0u, 0u, 0u, 0u);
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive(bar(P_FULL + group));
+                    mbar_arrive(bar(P_FULL + b));
                 if (plane && k * kTile + r < a.plan.lcap)
                     plane[k * kTile + r] = me.live ? wsum : 0.f;
             }
-            g0 += count;
+            it0 += count * halves;
+            const bool whole = w.k == 0 && count == w.z.kt;
+            // this group's half of the columns; the addend of a whole unit, before the wait
+            const int col0 = group * 64, nc = min(cols - col0, 64);
+            const int64_t at = ((w.s.s0 + q0 + col0 + (lane >> 2)) * c.H + h) * D + quarter * 32 + 8 * (lane & 3);
+            const int64_t eight = (int64_t)8 * c.H * D;  // eight queries on
+            uint4 add[8];
+            if (whole && a.addend && quarter * 32 < D)
+#pragma unroll
+                for (int i = 0; i < 8; i++)
+                    if (8 * i + (lane >> 2) < nc)
+                        add[i] = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.addend) + at + i * eight);
             if (!(ok = ok && wait(O_FULL, w.piece)))
                 break;
             tc_fence_after();
-            // O^T: lane = dim, column = query; this group's half of the columns
-            const bool whole = w.k == 0 && count == w.z.kt;
+            // O^T: lane = dim, column = query.  A whole unit leaves through the warp's own rows of
+            // a P^T buffer of its group, 32 queries x 32 dims at a time, so that memory sees
+            // 16-byte accesses.
             const int slot = w.k > 0 ? 0 : 1;
-            const int dim = r;
-            if (dim < D) {
+            if (quarter * 32 < D && nc > 0) {
+                unsigned char *stage = sm + LY::P + group * kPanel + quarter * 4096;
 #pragma unroll 1
-                for (int cc = group * 64; cc < min(cols, group * 64 + 64); cc += 16) {
+                for (int cc = 0; cc < nc; cc += 16) {
                     float ov[16];
-                    tmem_ld16(trow + 256 + cc, ov);
+                    tmem_ld16(trow + 256 + col0 + cc, ov);
                     tmem_wait_ld();
-                    const int m = min(16, cols - cc);
                     if (whole) {
-                        const int64_t at = ((w.s.s0 + q0 + cc) * c.H + h) * D + dim;
-                        const int step = c.H * D;
-                        __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + at;
 #pragma unroll
                         for (int e = 0; e < 16; e++)
-                            ov[e] *= a.inv_n;
-                        if (a.addend) {  // all loads before the stores: it may be `out`
-                            const __nv_bfloat16 *add = static_cast<const __nv_bfloat16 *>(a.addend) + at;
-                            __nv_bfloat16 y[16];
-#pragma unroll
-                            for (int e = 0; e < 16; e++)
-                                y[e] = add[(int64_t)min(e, m - 1) * step];
-#pragma unroll
-                            for (int e = 0; e < 16; e++)
-                                ov[e] += __bfloat162float(y[e]);
-                        }
-#pragma unroll
-                        for (int e = 0; e < 16; e++)
-                            if (e < m)
-                                out[(int64_t)e * step] = __float2bfloat16_rn(ov[e]);
+                            *reinterpret_cast<float *>(stage + ((cc & 16) + e) * 128 + (lane ^ ((e & 1) << 2)) * 4) = ov[e] * a.inv_n;
                     } else {
-                        float *part = a.part_o + ((int64_t)(2 * blockIdx.x + slot) * kTile + cc) * D + dim;
+                        float *part = a.part_o + ((int64_t)(2 * blockIdx.x + slot) * kTile + col0 + cc) * D + r;
 #pragma unroll
                         for (int e = 0; e < 16; e++)
-                            if (e < m)
+                            if (cc + e < nc)
                                 part[e * D] = ov[e];
+                    }
+                    if (whole && ((cc & 16) || cc + 16 >= nc)) {
+                        // 32 queries staged as floats: out they go
+                        __syncwarp();
+#pragma unroll
+                        for (int i4 = 0; i4 < 4; i4++) {
+                            const int qq = 8 * i4 + (lane >> 2), i = (cc >> 5) * 4 + i4;  // query of the half, of the 64 / 8
+                            const float *src = reinterpret_cast<const float *>(stage + qq * 128);
+                            const int x0 = (8 * (lane & 3)) ^ ((qq & 1) << 2);  // odd rows: fours swapped, against bank conflicts
+                            const float4 y0 = *reinterpret_cast<const float4 *>(src + x0);
+                            const float4 y1 = *reinterpret_cast<const float4 *>(src + (x0 ^ 4));
+                            if (8 * i + (lane >> 2) < nc) {
+                                float y[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
+                                if (a.addend) {
+                                    const uint4 ad = cc >> 5 ? add[4 + i4] : add[i4];
+                                    const uint32_t aw[4] = {ad.x, ad.y, ad.z, ad.w};
+#pragma unroll
+                                    for (int e = 0; e < 4; e++) {
+                                        y[2 * e] += __uint_as_float(aw[e] << 16);
+                                        y[2 * e + 1] += __uint_as_float(aw[e] & 0xffff0000u);
+                                    }
+                                }
+                                *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + at + i * eight) =
+                                    make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]),
+                                               pack_bf16(y[6], y[7]));
+                            }
+                        }
+                        __syncwarp();
                     }
                 }
             }

@@ -180,7 +180,7 @@ cudaError_t launch_cache_evict(const CacheCall &c, int keep, int first, int rece
 // two cut the key axis into `nsplit` parts of `split_pages` pages, whose sums go to
 // part_o [nsplit, T, H, d] (float32); the third cuts all its tiles into `ctas` runs,
 // with two slots [128, d] of part_o and two piece records each.  Where weights are
-// taken, each (query tile, head)'s go to a plane of part_w [planes, B, lcap].  A second
+// taken, those of plane_rows queries and one head go to a plane of part_w [planes, B, lcap].  A second
 // kernel joins them in a fixed order.
 constexpr int kCacheRows = 16;
 enum CacheKernel { CACHE_F32, CACHE_ROWS, CACHE_TC };
@@ -188,7 +188,8 @@ struct CacheAttnPlan {
     CacheKernel kernel;
     int nsplit, split_pages;
     int ctas;
-    int tile_rows, qtiles;  // query rows of a tile, tiles of a sequence
+    int qtiles;      // query tiles of a sequence (16 rows; 128 on the tensor cores)
+    int plane_rows;  // query rows of a plane (16; 64 on the tensor cores)
     int64_t lcap;
     size_t part_o_bytes, part_w_bytes, piece_bytes;
 };
