@@ -25,7 +25,7 @@
 // 256 P^T reads) alike; V^T as a TMEM operand is what keeps the last at 1024.
 //
 // Warp roles (512 threads): warp 0 loads the codes (TMA); warp 1 owns TMEM and issues
-// the MMAs (2 and 3 idle); warps 4-7 and 8-11 take the even and the odd tiles' S^T and
+// the MMAs (2 and 3 idle); warps 4-19, in four groups,
 // write P^T; warps 12-15 split queries and convert values.
 // TMEM columns: S^T [0, 128) and [128, 256), O^T [256, 384), V^T [384, 448), [448, 512).
 //
@@ -46,15 +46,26 @@ namespace hstu {
 namespace {
 
 constexpr int kTile = 128;    // keys of a tile, query columns of a unit
-constexpr int kThreads = 512;
+constexpr int kThreads = 896;
 constexpr int kKStages = 3, kVStages = 2;  // tiles of codes in flight
 constexpr int kCutTiles = 8;  // what a cut unit costs (its pieces' traffic and the join), in tiles
 constexpr int kPanel = 16384; // 64 query columns of P^T: 128 keys x 128 bytes
 
+constexpr int kKeySlots = 4;  // tiles of key data ahead
+
 enum Bars { K_FULL = 0, K_EMPTY = K_FULL + kKStages, C_FULL = K_EMPTY + kKStages, C_EMPTY = C_FULL + kVStages,
-            S_FULL = C_EMPTY + kVStages, P_FULL = S_FULL + 4, P_EMPTY = P_FULL + 4, V_FULL = P_EMPTY + 4,
-            V_EMPTY = V_FULL + 2, Q_FULL = V_EMPTY + 2, Q_EMPTY = Q_FULL + 2, O_FULL = Q_EMPTY + 2,
-            O_FREE = O_FULL + 1, NBARS = O_FREE + 1 };
+            S_FULL = C_EMPTY + kVStages, P_FULL = S_FULL + 4, V_FULL = P_FULL + 4,
+            V_EMPTY = V_FULL + 2, KEY_FULL = V_EMPTY + 2, KEY_EMPTY = KEY_FULL + kKeySlots,
+            Q_FULL = KEY_EMPTY + kKeySlots, Q_EMPTY = Q_FULL + 2, O_FULL = Q_EMPTY + 2, O_FREE = O_FULL + 1,
+            NBARS = O_FREE + 1 };
+
+// what the epilogue needs to know of a tile's keys: the bias against column 0 and the scale, both halved (scale -1:
+// no token), position and stamp
+struct KeyInfo {
+    float2 bias_scale[kTile];
+    int pos[kTile];
+    int64_t ts[kTile];
+};
 
 // what the epilogue needs to know of a unit's queries
 struct QueryInfo {
@@ -75,7 +86,8 @@ struct Layout {
     static constexpr int V = K + kKStages * KT;  // value codes [2 pages][D][64]
     static constexpr int P = V + kVStages * KT;
     static constexpr int INFO = P + 4 * kPanel;
-    static constexpr int BAR = INFO + 2 * (int)sizeof(QueryInfo);
+    static constexpr int KEYS = INFO + 2 * (int)sizeof(QueryInfo);
+    static constexpr int BAR = KEYS + kKeySlots * (int)sizeof(KeyInfo);
     static constexpr int MISC = BAR + NBARS * 8;
     static constexpr int BYTES = MISC + 128 + 1024;
     static_assert(BYTES <= 227 * 1024, "shared memory of an SM");
@@ -243,34 +255,6 @@ __device__ __forceinline__ uint32_t pow2_bf16x2(int e)  // two copies of 2^e, -1
 // SiLU(2 h)
 __device__ __forceinline__ float silu_half(float h) { return fmaf(h, tanh_approx(h), h); }
 
-// mbar_wait, but asleep until the phase ends (the hint: 1 ms at most) instead of
-// polling: ten waiting warps would take a third of the issue slots.
-__device__ __forceinline__ bool sleep_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag, WsHeader *hdr)
-{
-    auto try_wait = [&] {
-        uint32_t done;
-        asm volatile(
-            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
-            : "=r"(done)
-            : "r"(bar), "r"(parity), "r"(1000000u)
-            : "memory");
-        return done != 0;
-    };
-    if (try_wait())
-        return true;
-    const long long t0 = clock64();
-    while (!try_wait()) {
-        if (*abort_flag)
-            return false;
-        if (clock64() - t0 > kWaitLimitCycles) {
-            *abort_flag = 1;
-            atomicOr(&hdr->flag, FLAG_TIMEOUT);
-            return false;
-        }
-    }
-    return true;
-}
-
 // One lane of a converged warp.  Under this predicate the compiler knows that one thread
 // issues; under `lane == 0` it wraps every TMA, MMA and commit in a loop over the active
 // lanes, which took 100 cycles an MMA.
@@ -358,6 +342,9 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
     auto bar = [&](int i) { return base + LY::BAR + 8u * i; };
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + LY::MISC + 8);
     QueryInfo *info = reinterpret_cast<QueryInfo *>(sm + LY::INFO);
+    KeyInfo *keys = reinterpret_cast<KeyInfo *>(sm + LY::KEYS);
+
+    int2 *v_scales = reinterpret_cast<int2 *>(sm + LY::MISC + 48);  // of the tiles in the value ring, as bits
 
     int64_t *found = reinterpret_cast<int64_t *>(sm + LY::MISC + 16);
     const bool work = find_run(c, blockIdx.x, gridDim.x, reinterpret_cast<int64_t *>(sm + LY::P), found);
@@ -376,18 +363,22 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
     if (threadIdx.x == 0) {
         for (int i = 0; i < NBARS; i++) {
             int n = 1;
-            if ((i >= P_FULL && i < P_FULL + 4) || i == Q_FULL || i == Q_FULL + 1)
+            if (i >= S_FULL && i < S_FULL + 4)
+                n = 2;  // S^T is there, and P^T of the item four back has been read
+            else if ((i >= P_FULL && i < P_FULL + 4) || i == Q_FULL || i == Q_FULL + 1)
                 n = 4;
             else if (i == V_FULL || i == V_FULL + 1 || (i >= C_EMPTY && i < C_EMPTY + kVStages))
                 n = D / 32;
             else if (i == Q_EMPTY || i == Q_EMPTY + 1)
-                n = 9;
+                n = 18;
             else if (i == O_FREE)
-                n = 8;
+                n = 16;
             mbar_init(bar(i), n);
         }
         *abort_flag = 0;
         fence_mbar_init();
+        for (int i = 0; i < 4; i++)  // nothing to read before the first items
+            mbar_arrive(bar(S_FULL + i));
         tma_prefetch(&tk);
         tma_prefetch(&tv);
     }
@@ -398,8 +389,7 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(sm + LY::MISC);
     bool ok = true;
-    auto wait = [&](int i, int parity) { return sleep_wait(bar(i), parity & 1, abort_flag, hdr); };
-
+    auto wait = [&](int i, int parity) { return mbar_wait(bar(i), parity & 1, abort_flag, hdr); };
     // by a whole warp that stays converged
     auto wait_all = [&](int i, int parity) { return __all_sync(0xffffffffu, wait(i, parity)) != 0; };
 
@@ -408,7 +398,7 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
         int g = 0;
         for (Walk w = start; ok && w.left > 0; w.next(c)) {
             const int h = w.head(), pages = (w.s.len + kPage - 1) / kPage, count = w.count();
-            int held = -1;  // lane: a page of this and the next 15 tiles
+            int held = -1, held_scale = 0;  // lane: a page of this and the next 15 tiles, its v_scale's bits
             for (int t = 0; t < count; t++, g++) {
                 const int k = w.k + t, kst = g % kKStages, vst = g % kVStages;
                 if (t % 16 == 0) {
@@ -418,9 +408,12 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
                         if (held < 0)
                             atomicOr(&hdr->flag, FLAG_CACHE_PAGE);
                     }
+                    held_scale = held >= 0 ? __float_as_int(c.v_scale[(int64_t)held * c.H + h]) : 0;
                 }
                 const int page[2] = {__shfl_sync(0xffffffffu, held, 2 * (t % 16)),
                                      __shfl_sync(0xffffffffu, held, 2 * (t % 16) + 1)};
+                const int sc0 = __shfl_sync(0xffffffffu, held_scale, 2 * (t % 16));
+                const int sc1 = __shfl_sync(0xffffffffu, held_scale, 2 * (t % 16) + 1);
                 const uint32_t bytes = ((page[0] >= 0) + (page[1] >= 0)) * kPage * D;
                 ok = g < kKStages || wait_all(K_EMPTY + kst, g / kKStages - 1);
                 if (!ok)
@@ -437,6 +430,7 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
                 if (!ok)
                     break;
                 if (elect_one()) {
+                    v_scales[vst] = make_int2(sc0, sc1);
                     mbar_expect_tx(bar(C_FULL + vst), bytes);
 #pragma unroll
                     for (int e = 0; e < 2; e++)
@@ -456,7 +450,8 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
                 break;
             for (int t = 0; ok && t < count; t++, g++) {
                 const int st = g % kKStages;
-                if (!(ok = wait_all(K_FULL + st, g / kKStages)))
+                // the key data too: S_FULL then stands for both
+                if (!(ok = wait_all(K_FULL + st, g / kKStages) && wait_all(KEY_FULL + g % kKeySlots, g / kKeySlots)))
                     break;
                 // both halves at once where their buffers are neighbours
                 const int wide = halves == 2 && (it & 1) == 0 ? 2 : 1;
@@ -510,8 +505,9 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
                         for (int ks = 0; ks < kTile / 16; ks++)  // 16 rows of P^T a step
                             umma_bf16_ts(tmem + 256 + hf * 64, tmem + 384 + vb * 64 + ks * 8, pd + ks * (2048 >> 4), id,
                                          ks > 0 || t > 0);
-                        umma_commit(bar(P_EMPTY + (it & 3)));
+                        umma_commit(bar(S_FULL + (it & 3)));
                         if (hf + 1 == halves) {
+                            mbar_arrive(bar(KEY_EMPTY + g % kKeySlots));  // every P^T of the tile is there
                             umma_commit(bar(V_EMPTY + vb));
                             if (t + 1 == count)
                                 umma_commit(bar(O_FULL));
@@ -521,16 +517,91 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
                 }
             }
         }
-    } else if (warp >= 12) {
-        // ---------------- queries and values ----------------
-        const int quarter = warp & 3, dim = quarter * 32 + lane;
-        const int row = threadIdx.x - 384;  // of the queries
+    } else if (warp == 3) {
+        // ---------------- keys' biases ----------------
+        // four keys a lane; what a tile needs is fetched ahead, one step of the chain a tile: the
+        // pages, the tokens' positions, stamps and scales, the biases
         int g = 0;
         for (Walk w = start; ok && w.left > 0; w.next(c)) {
-            const int qs = w.piece & 1, h = w.head(), q0 = w.q0(), cols = w.cols();
-            if (w.piece >= 2 && !(ok = wait(Q_EMPTY + qs, (w.piece >> 1) - 1)))
+            const int qs = w.piece & 1, h = w.head(), count = w.count();
+            const float *rp = a.rab_pos + h * a.pos_hstride, *rt = a.rab_time + h * a.time_hstride;
+            struct Keys {
+                int pos[4];
+                int64_t ts[4];
+                float scale[4];  // -1: no token
+            };
+            int page[2];
+            auto pages_at = [&](int t) {
+#pragma unroll
+                for (int e = 0; e < 2; e++) {
+                    const int p = 2 * (w.k + t) + e;
+                    page[e] = t < count && p * kPage < w.s.len ? table_page(c.table, c, w.b, p) : -1;
+                }
+            };
+            auto keys_at = [&](int t, Keys &y) {
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const int r = 32 * i + lane, id = page[i >> 1];
+                    const bool live = id >= 0 && (w.k + t) * kTile + r < w.s.len;
+                    const int64_t at = live ? (int64_t)id * kPage + r % kPage : 0;
+                    y.pos[i] = c.positions[at];
+                    y.ts[i] = c.timestamps[at];
+                    y.scale[i] = live ? c.k_scale[(int64_t)id * c.H + h] : -2.f;
+                }
+            };
+            float bp[4], bt[4];
+            Keys now, next;
+            pages_at(0);
+            keys_at(0, now);
+            pages_at(1);
+            if (!(ok = wait_all(Q_FULL + qs, w.piece >> 1)))
                 break;
-            {
+            const int p_i = info[qs].pos[0];
+            const int64_t t_i = info[qs].ts[0];
+            auto biases = [&](const Keys &y) {
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    bp[i] = rp[pos_index(p_i, y.pos[i], a.pos_lo, a.pos_hi)];
+                    bt[i] = rt[time_bucket(t_i, y.ts[i], a.nb)];
+                }
+            };
+            biases(now);
+            keys_at(1, next);
+            pages_at(2);
+            for (int t = 0; t < count; t++, g++) {
+                const int slot = g % kKeySlots;
+                if (g >= kKeySlots && !(ok = wait_all(KEY_EMPTY + slot, g / kKeySlots - 1)))
+                    break;
+                KeyInfo &ki = keys[slot];
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    ki.bias_scale[32 * i + lane] = make_float2(0.5f * (bp[i] + bt[i]), 0.5f * now.scale[i]);
+                    ki.pos[32 * i + lane] = now.pos[i];
+                    ki.ts[32 * i + lane] = now.ts[i];
+                }
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(bar(KEY_FULL + slot));
+                biases(next);
+                now = next;
+                keys_at(t + 2, next);
+                pages_at(t + 3);
+            }
+            if (lane == 0 && ok)
+                mbar_arrive(bar(Q_EMPTY + qs));
+        }
+    } else if (warp >= 20) {
+        // ---------------- queries and values ----------------
+        const int quarter = warp & 3, dim = quarter * 32 + lane;
+        // two groups of four warps: a group splits every other unit's queries and converts
+        // every other tile
+        const int group = (warp - 20) >> 2, row = threadIdx.x - 640 - 128 * group;  // of the queries
+        int g0 = 0;
+        for (Walk w = start; ok && w.left > 0; w.next(c)) {
+            const int qs = w.piece & 1, h = w.head(), q0 = w.q0(), cols = w.cols();
+            if (qs == group) {
+                if (w.piece >= 2 && !(ok = wait(Q_EMPTY + qs, (w.piece >> 1) - 1)))
+                    break;
                 QueryInfo &qi = info[qs];
                 // LR lanes a row, eight elements a lane.  The row passes through the places of
                 // its two parts (eight bytes a lane in each), read back by the lane that wrote.
@@ -569,20 +640,21 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
                     return m;
                 };
                 uint32_t all = 0, least = 0xffffffffu;
-                {
-                    uint4 x[LR];
+#pragma unroll 1
+                for (int j0 = 0; j0 < LR; j0 += 8) {
+                    uint4 x[8];
 #pragma unroll
-                    for (int j = 0; j < LR; j++) {
-                        const int rr = 32 * chunk + RI * j + lr;
+                    for (int j = 0; j < 8; j++) {
+                        const int rr = 32 * chunk + RI * (j0 + j) + lr;
                         x[j] = rr < cols ? *reinterpret_cast<const uint4 *>(qp + rr * a.ldq) : make_uint4(0u, 0u, 0u, 0u);
                     }
 #pragma unroll
-                    for (int j = 0; j < LR; j++) {
+                    for (int j = 0; j < 8; j++) {
                         const uint32_t ww[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
                         const uint32_t m = row_max(ww);
                         all = max(all, m);
                         least = min(least, m ? m : 0xffffffffu);
-                        unsigned char *at = place(32 * chunk + RI * j + lr);
+                        unsigned char *at = place(32 * chunk + RI * (j0 + j) + lr);
                         *reinterpret_cast<uint2 *>(at) = make_uint2(ww[0], ww[1]);
                         *reinterpret_cast<uint2 *>(at + LY::KT) = make_uint2(ww[2], ww[3]);
                     }
@@ -628,255 +700,205 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
                 if (lane == 0)
                     mbar_arrive(bar(Q_FULL + qs));
             }
-            if (dim >= D) {  // d = 64 has half the rows of V^T
-                g += w.count();
-                continue;
-            }
             const int count = w.count();
-            // scale bits of page 2 k + e, 0 for none; its page id one tile earlier
-            auto page_at = [&](int p) { return p * kPage < w.s.len ? table_page(c.table, c, w.b, p) : -1; };
-            auto scale_at = [&](int page) {
-                return page >= 0 ? __float_as_int(c.v_scale[(int64_t)page * c.H + h]) : 0;
-            };
-            int ids[2], sc[2];
-#pragma unroll
-            for (int e = 0; e < 2; e++) {
-                sc[e] = scale_at(page_at(2 * w.k + e));
-                ids[e] = count > 1 ? page_at(2 * w.k + 2 + e) : -1;
-            }
-            for (int t = 0; t < count; t++, g++) {
-                const int k = w.k + t, vb = g & 1, vst = g % kVStages;
-                int next[2];
-#pragma unroll
-                for (int e = 0; e < 2; e++) {
-                    next[e] = t + 1 < count ? scale_at(ids[e]) : 0;
-                    ids[e] = t + 2 < count ? page_at(2 * k + 4 + e) : -1;
-                }
-                if (!(ok = wait(C_FULL + vst, g / kVStages) && (g < 2 || wait(V_EMPTY + vb, (g >> 1) - 1))))
+            for (int t = (g0 ^ group) & 1; dim < D && t < count; t += 2) {  // d = 64 has half the rows of V^T
+                const int g = g0 + t, k = w.k + t;
+                if (!(ok = wait(C_FULL + group, g >> 1) && (g < 2 || wait(V_EMPTY + group, (g >> 1) - 1))))
                     break;
+                const int2 sc = v_scales[group];
                 tc_fence_after();
-                // 32 keys at a time, rolled: the roles' loops share the instruction cache
-                const unsigned char *vrow = sm + LY::V + vst * LY::KT + dim * kPage;
-                const uint32_t dst = tmem + ((uint32_t)(quarter * 32) << 16) + 384 + vb * 64;
+                const unsigned char *vrow = sm + LY::V + group * LY::KT + dim * kPage;
+                const uint32_t dst = tmem + ((uint32_t)(quarter * 32) << 16) + 384 + group * 64;
+                auto codes = [&](int i) {  // 16 keys of the tile
+                    return *reinterpret_cast<const uint4 *>(vrow + (i >> 2) * kPage * D + ((i & 3) ^ ((dim >> 1) & 3)) * 16);
+                };
+                // times the scale 2^x and the 2^120 that the conversion leaves out: one factor
+                // where bf16 has 2^(120 + x)
+                const int x0 = (sc.x >> 23 & 255) - 127, x1 = (sc.y >> 23 & 255) - 127;
+                const bool plain = (k + 1) * kTile <= w.s.len && sc.x != 0 && sc.y != 0 && max(x0, x1) <= 7;
+                if (plain) {
+                    uint4 v[8];
+#pragma unroll
+                    for (int i = 0; i < 8; i++)
+                        v[i] = codes(i);
+#pragma unroll
+                    for (int q = 0; q < 4; q++) {
+                        const uint32_t f = pow2_bf16x2(120 + (q < 2 ? x0 : x1));
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int i = 0; i < 8; i++) {
+                            const uint4 &y = v[2 * q + (i >> 2)];
+                            const uint32_t c4 = (i & 3) == 0 ? y.x : (i & 3) == 1 ? y.y : (i & 3) == 2 ? y.z : y.w;
+                            pk[2 * i] = mul_bf16x2(even_codes(c4), f);
+                            pk[2 * i + 1] = mul_bf16x2(odd_codes(c4), f);
+                        }
+                        tmem_st16(dst + 16 * q, pk);
+                    }
+                } else {
+                    // a ragged or missing page (codes there may be anything), a scale of 0, NaN or
+                    // above 2^7: two factors, a NaN scale as it is
 #pragma unroll 1
-                for (int q = 0; q < 4; q++) {
-                    const int e = q >> 1, n = w.s.len - k * kTile - 32 * q, bits = e ? sc[1] : sc[0];
-                    const unsigned char *src = vrow + e * kPage * D;
-                    uint32_t v[8];
+                    for (int q = 0; q < 4; q++) {
+                        const int bits = q < 2 ? sc.x : sc.y, x = q < 2 ? x0 : x1;
+                        const int n = bits == 0 ? 0 : w.s.len - k * kTile - 32 * q;
+                        const int e1 = x == 128 ? 120 : min(120 + max(x, -126), 127);
+                        const uint32_t f1 = pow2_bf16x2(e1);
+                        const uint32_t f2 = x == 128 ? 0x7fff7fffu : pow2_bf16x2(max(120 + x - e1, 0));
+                        const uint4 y0 = codes(2 * q), y1 = codes(2 * q + 1);
+                        const uint32_t c8[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
+                        uint32_t pk[16];
 #pragma unroll
-                    for (int i = 0; i < 2; i++) {
-                        const uint4 y = *reinterpret_cast<const uint4 *>(src + ((2 * (q & 1) + i) ^ ((dim >> 1) & 3)) * 16);
-                        v[4 * i] = y.x, v[4 * i + 1] = y.y, v[4 * i + 2] = y.z, v[4 * i + 3] = y.w;
+                        for (int i = 0; i < 8; i++) {
+                            const uint32_t c4 = n >= 4 * i + 4 ? c8[i] : n <= 4 * i ? 0u : c8[i] & ((1u << (8 * (n - 4 * i))) - 1u);
+                            pk[2 * i] = mul_bf16x2(mul_bf16x2(even_codes(c4), f1), f2);
+                            pk[2 * i + 1] = mul_bf16x2(mul_bf16x2(odd_codes(c4), f1), f2);
+                        }
+                        tmem_st16(dst + 16 * q, pk);
                     }
-                    // codes behind the last token, or of a page that was not loaded, may be anything
-                    if (n < 32 || bits == 0) {
-                        const int keep = bits == 0 ? 0 : n;
-#pragma unroll
-                        for (int i = 0; i < 8; i++)
-                            v[i] = keep >= 4 * i + 4 ? v[i] : keep <= 4 * i ? 0u : v[i] & ((1u << (8 * (keep - 4 * i))) - 1u);
-                    }
-                    // times the scale 2^x and 2^120, in two factors where bf16 has no 2^(120 + x); a NaN scale as it is
-                    const int x = (bits >> 23 & 255) - 127;
-                    const bool nan = x == 128;
-                    const int x1 = nan ? 120 : min(120 + max(x, -126), 127);
-                    const uint32_t f1 = pow2_bf16x2(x1);
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int i = 0; i < 8; i++) {
-                        pk[2 * i] = mul_bf16x2(even_codes(v[i]), f1);
-                        pk[2 * i + 1] = mul_bf16x2(odd_codes(v[i]), f1);
-                    }
-                    if (nan || 120 + x > 127) {
-                        const uint32_t f2 = nan ? 0x7fff7fffu : pow2_bf16x2(max(120 + x - x1, 0));
-#pragma unroll
-                        for (int i = 0; i < 16; i++)
-                            pk[i] = mul_bf16x2(pk[i], f2);
-                    }
-                    tmem_st16(dst + 16 * q, pk);
                 }
-                sc[0] = next[0], sc[1] = next[1];
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(bar(C_EMPTY + vst));
-                    mbar_arrive(bar(V_FULL + vb));
+                    mbar_arrive(bar(C_EMPTY + group));
+                    mbar_arrive(bar(V_FULL + group));
                 }
             }
+            g0 += count;
         }
     } else if (warp >= 4) {
         // ---------------- S^T to P^T ----------------
         const int group = (warp - 4) >> 2, quarter = warp & 3;
         const int r = quarter * 32 + lane, row_p = key_row(r);  // key of the tile, its row of P^T
-        const uint32_t trow = tmem + ((uint32_t)(quarter * 32) << 16);
-        int it0 = 0;  // items before this piece
+        const uint32_t trow = tmem + ((uint32_t)(quarter * 32) << 16), taddr = trow + group * 64;
+        unsigned char *prow = sm + LY::P + group * kPanel + row_p * 128;
+        int it0 = 0, g0 = 0;  // items and tiles before this piece
         for (Walk w = start; ok && w.left > 0; w.next(c)) {
             const int qs = w.piece & 1, h = w.head(), q0 = w.q0(), cols = w.cols(), count = w.count();
             const float *rp = a.rab_pos + h * a.pos_hstride, *rt = a.rab_time + h * a.time_hstride;
             const QueryInfo &qi = info[qs];
-            // Items (a tile's 64 columns) alternate between the groups: of a tile with two,
-            // each group takes one; of tiles with one, every other tile.
-            const int halves = cols > 64 ? 2 : 1, step = halves == 2 ? 1 : 2;
-            const int first = halves == 2 ? 0 : (it0 ^ group) & 1, hf = halves == 2 ? (it0 ^ group) & 1 : 0;
+            // Items (a tile's 64 columns) go round the groups; a group keeps its buffer, and
+            // within a unit its half.
+            const int halves = cols > 64 ? 2 : 1, i0 = (group - it0) & 3;  // the group's first item here
+            const int hf = halves == 2 ? i0 & 1 : 0, first = halves == 2 ? i0 >> 1 : i0, step = 4 / halves;
             const int c0 = hf * 64, n = min(cols - c0, 64);
             float *plane =
                 a.part_w ? a.part_w + ((int64_t)((q0 + c0) / 64 * c.H + h) * c.B + w.b) * a.plan.lcap : nullptr;
-            // What a tile needs of this thread's key is fetched ahead, one step of the chain a
-            // tile: the page, the token's position, stamp and scale, the bias of column 0.
-            struct Key {
-                bool live;
-                int pos;
-                int64_t ts;
-                float scale;
-            };
-            auto page_at = [&](int t) {
-                const int j = (w.k + t) * kTile + r;
-                return t < count && j < w.s.len ? table_page(c.table, c, w.b, j / kPage) : -1;
-            };
-            auto key_at = [&](int page) {
-                Key y{page >= 0, 0, 0, 0.f};
-                if (y.live) {
-                    const int64_t at = (int64_t)page * kPage + r % kPage;
-                    y.pos = c.positions[at];
-                    y.ts = c.timestamps[at];
-                    y.scale = c.k_scale[(int64_t)page * c.H + h];
-                }
-                return y;
-            };
-            Key key = key_at(page_at(first)), ahead = key_at(page_at(first + step));
-            int page = page_at(first + 2 * step);
             if (!(ok = wait(Q_FULL + qs, w.piece >> 1)))
                 break;
-            const int p_i = qi.pos[0], ch = c0 >> 5, ch1 = n > 32 ? ch + 1 : ch;
-            const int64_t t_i = qi.ts[0];
+            const int ch = c0 >> 5, ch1 = n > 32 ? ch + 1 : ch;
             const float s0 = qi.chunk_scale[ch], s1 = qi.chunk_scale[ch1];
-            const bool same = qi.chunk_same[ch] && qi.chunk_same[ch1] && s0 != -1.f && s1 != -1.f &&
-                              (!plane || n % 32 == 0);
-            float bp = 0.f, bt = 0.f;
-            if (key.live) {
-                bp = rp[pos_index(p_i, key.pos, a.pos_lo, a.pos_hi)];
-                bt = rt[time_bucket(t_i, key.ts, a.nb)];
-            }
+            const bool same = qi.chunk_same[ch] && qi.chunk_same[ch1] && s0 != -1.f && s1 != -1.f;
             for (int t = first; t < count; t += step) {
-                const int it = it0 + (halves == 2 ? 2 * t + hf : t), k = w.k + t, b = it & 3;
-                const Key me = key;
-                const float bias = 0.5f * (bp + bt), half_scale = 0.5f * me.scale;
-                key = ahead;
-                bp = bt = 0.f;
-                if (key.live) {
-                    bp = rp[pos_index(p_i, key.pos, a.pos_lo, a.pos_hi)];
-                    bt = rt[time_bucket(t_i, key.ts, a.nb)];
-                }
-                ahead = key_at(page);
-                page = page_at(t + 3 * step);
-                if (!(ok = wait(S_FULL + b, it >> 2) && (it < 4 || wait(P_EMPTY + b, (it >> 2) - 1))))
+                const int it = it0 + halves * t + hf, k = w.k + t, slot = (g0 + t) % kKeySlots;
+                if (!(ok = wait(S_FULL + group, it >> 2)))
                     break;
                 tc_fence_after();
+                const float2 bs = keys[slot].bias_scale[r];
+                const bool live = bs.y != -1.f;
                 float wsum = 0.f;
-                unsigned char *prow = sm + LY::P + b * kPanel + row_p * 128;
-                const uint32_t taddr = trow + b * 64;
                 if (same) {
 #pragma unroll 1
                     for (int q = 0; 32 * q < n; q++) {
                         float x[32];
                         tmem_ld32(taddr + 32 * q, x);
                         tmem_wait_ld();
-                        const float f = half_scale * (q ? s1 : s0);
+                        const float f = bs.y * (q ? s1 : s0);
 #pragma unroll
                         for (int e = 0; e < 32; e++)
-                            x[e] = silu_half(fmaf(x[e], f, bias));
+                            x[e] = silu_half(fmaf(x[e], f, bs.x));
 #pragma unroll
                         for (int e = 0; e < 4; e++)
                             put_p8(x + 8 * e, prow + ((4 * q + e) ^ (row_p & 7)) * 16);
                         if (plane) {
                             float w0 = 0.f, w1 = 0.f;
+                            if (n >= 32 * q + 32) {
 #pragma unroll
-                            for (int e = 0; e < 32; e += 2)
-                                w0 += fabsf(x[e]), w1 += fabsf(x[e + 1]);
+                                for (int e = 0; e < 32; e += 2)
+                                    w0 += fabsf(x[e]), w1 += fabsf(x[e + 1]);
+                            } else {
+#pragma unroll
+                                for (int e = 0; e < 32; e++)
+                                    w0 += 32 * q + e < n ? fabsf(x[e]) : 0.f;
+                            }
                             wsum += w0 + w1;
                         }
                     }
                 } else {
+                    const int pj = keys[slot].pos[r];
+                    const int64_t tj = keys[slot].ts[r];
                     for (int cc = 0; cc < n; cc += 32)
-                        wsum += chunk_general(taddr + cc, c0 + cc, n - cc, a, rp, rt, qi, me.live, me.pos, me.ts,
-                                              half_scale, prow, row_p);
+                        wsum += chunk_general(taddr + cc, c0 + cc, n - cc, a, rp, rt, qi, live, pj, tj, bs.y, prow, row_p);
                 }
-                if (!me.live)  // no token, and S^T of whatever the tile holds there: P is 0
+                if (!live)  // no token, and S^T of whatever the tile holds there: P is 0
                     for (int e = 0; e < 8; e++)
                         *reinterpret_cast<uint4 *>(prow + e * 16) = make_uint4(0u, 0u, 0u, 0u);
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive(bar(P_FULL + b));
+                    mbar_arrive(bar(P_FULL + group));
                 if (plane && k * kTile + r < a.plan.lcap)
-                    plane[k * kTile + r] = me.live ? wsum : 0.f;
+                    plane[k * kTile + r] = live ? wsum : 0.f;
             }
+            g0 += count;
             it0 += count * halves;
             const bool whole = w.k == 0 && count == w.z.kt;
-            // this group's half of the columns; the addend of a whole unit, before the wait
-            const int col0 = group * 64, nc = min(cols - col0, 64);
+            // this group's quarter of the columns; the addend of a whole unit, before the wait
+            const int col0 = group * 32, nc = min(cols - col0, 32);
             const int64_t at = ((w.s.s0 + q0 + col0 + (lane >> 2)) * c.H + h) * D + quarter * 32 + 8 * (lane & 3);
             const int64_t eight = (int64_t)8 * c.H * D;  // eight queries on
-            uint4 add[8];
+            uint4 add[4];
             if (whole && a.addend && quarter * 32 < D)
 #pragma unroll
-                for (int i = 0; i < 8; i++)
+                for (int i = 0; i < 4; i++)
                     if (8 * i + (lane >> 2) < nc)
                         add[i] = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.addend) + at + i * eight);
             if (!(ok = ok && wait(O_FULL, w.piece)))
                 break;
             tc_fence_after();
             // O^T: lane = dim, column = query.  A whole unit leaves through the warp's own rows of
-            // a P^T buffer of its group, 32 queries x 32 dims at a time, so that memory sees
-            // 16-byte accesses.
+            // its P^T buffer, 32 queries x 32 dims, so that memory sees 16-byte accesses.
             const int slot = w.k > 0 ? 0 : 1;
             if (quarter * 32 < D && nc > 0) {
                 unsigned char *stage = sm + LY::P + group * kPanel + quarter * 4096;
-#pragma unroll 1
-                for (int cc = 0; cc < nc; cc += 16) {
-                    float ov[16];
-                    tmem_ld16(trow + 256 + col0 + cc, ov);
-                    tmem_wait_ld();
-                    if (whole) {
+                float ov[32];
+                tmem_ld32(trow + 256 + col0, ov);
+                tmem_wait_ld();
+                if (!whole) {
+                    float *part = a.part_o + ((int64_t)(2 * blockIdx.x + slot) * kTile + col0) * D + r;
 #pragma unroll
-                        for (int e = 0; e < 16; e++)
-                            *reinterpret_cast<float *>(stage + ((cc & 16) + e) * 128 + (lane ^ ((e & 1) << 2)) * 4) = ov[e] * a.inv_n;
-                    } else {
-                        float *part = a.part_o + ((int64_t)(2 * blockIdx.x + slot) * kTile + col0 + cc) * D + r;
+                    for (int e = 0; e < 32; e++)
+                        if (e < nc)
+                            part[e * D] = ov[e];
+                } else {
+                    // odd queries with fours of dims swapped, against bank conflicts
 #pragma unroll
-                        for (int e = 0; e < 16; e++)
-                            if (cc + e < nc)
-                                part[e * D] = ov[e];
-                    }
-                    if (whole && ((cc & 16) || cc + 16 >= nc)) {
-                        // 32 queries staged as floats: out they go
-                        __syncwarp();
+                    for (int e = 0; e < 32; e++)
+                        *reinterpret_cast<float *>(stage + e * 128 + (lane ^ ((e & 1) << 2)) * 4) = ov[e] * a.inv_n;
+                    __syncwarp();
 #pragma unroll
-                        for (int i4 = 0; i4 < 4; i4++) {
-                            const int qq = 8 * i4 + (lane >> 2), i = (cc >> 5) * 4 + i4;  // query of the half, of the 64 / 8
-                            const float *src = reinterpret_cast<const float *>(stage + qq * 128);
-                            const int x0 = (8 * (lane & 3)) ^ ((qq & 1) << 2);  // odd rows: fours swapped, against bank conflicts
-                            const float4 y0 = *reinterpret_cast<const float4 *>(src + x0);
-                            const float4 y1 = *reinterpret_cast<const float4 *>(src + (x0 ^ 4));
-                            if (8 * i + (lane >> 2) < nc) {
-                                float y[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
-                                if (a.addend) {
-                                    const uint4 ad = cc >> 5 ? add[4 + i4] : add[i4];
-                                    const uint32_t aw[4] = {ad.x, ad.y, ad.z, ad.w};
+                    for (int i = 0; i < 4; i++) {
+                        const int qq = 8 * i + (lane >> 2), x0 = (8 * (lane & 3)) ^ ((qq & 1) << 2);
+                        const float *src = reinterpret_cast<const float *>(stage + qq * 128);
+                        const float4 y0 = *reinterpret_cast<const float4 *>(src + x0);
+                        const float4 y1 = *reinterpret_cast<const float4 *>(src + (x0 ^ 4));
+                        if (qq < nc) {
+                            float y[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
+                            if (a.addend) {
+                                const uint32_t aw[4] = {add[i].x, add[i].y, add[i].z, add[i].w};
 #pragma unroll
-                                    for (int e = 0; e < 4; e++) {
-                                        y[2 * e] += __uint_as_float(aw[e] << 16);
-                                        y[2 * e + 1] += __uint_as_float(aw[e] & 0xffff0000u);
-                                    }
+                                for (int e = 0; e < 4; e++) {
+                                    y[2 * e] += __uint_as_float(aw[e] << 16);
+                                    y[2 * e + 1] += __uint_as_float(aw[e] & 0xffff0000u);
                                 }
-                                *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + at + i * eight) =
-                                    make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]),
-                                               pack_bf16(y[6], y[7]));
                             }
+                            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + at + i * eight) =
+                                make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]),
+                                           pack_bf16(y[6], y[7]));
                         }
-                        __syncwarp();
                     }
+                    __syncwarp();
                 }
             }
             tc_fence_before();
