@@ -69,10 +69,10 @@ struct KeyInfo {
 
 // what the epilogue needs to know of a unit's queries
 struct QueryInfo {
-    float chunk_scale[4];  // one scale of the 32 columns, or -1: each its own
-    int chunk_same[4];     // every column has row 0's position and stamp
-    int pos_lo[4], pos_hi[4];  // a chunk's least and largest position and stamp
-    int64_t ts_lo[4], ts_hi[4];
+    float chunk_scale[8];  // one scale of 16 columns, or -1: each its own
+    int chunk_same[8];     // every column has row 0's position and stamp
+    int pos_lo[8], pos_hi[8];  // a chunk's least and largest position and stamp
+    int64_t ts_lo[8], ts_hi[8];
     float scale[kTile];
     int pos[kTile];
     int64_t ts[kTile];
@@ -188,7 +188,7 @@ __device__ bool find_run(const CacheCall &c, int cta, int ctas, int64_t *sums, i
     }
     __syncthreads();
     int64_t before = 0, total = 0;
-    for (int w = 0; w < kW; w++) {
+    for (int w = 0; w < min(kW, (c.B + 32 * per - 1) / (32 * per)); w++) {
         if (w < warp)
             before += sums[w];
         total += sums[w];
@@ -281,21 +281,21 @@ __device__ __forceinline__ void put_p8(const float *x, unsigned char *dst)
         make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
 }
 
-// A chunk of 32 queries whose biases or scales differ: this key's P^T, and the sum of
+// A chunk of 16 queries whose biases or scales differ: this key's P^T, and the sum of
 // its magnitudes over the first n.  Where the whole warp's pairs share an index of a
 // table, it is read once.  Eight queries at a time: the common loop keeps its registers.
 __device__ __forceinline__ float chunk_general(uint32_t taddr, int cc, int n, const CacheAttnArgs &a, const float *rp,
                                                const float *rt, const QueryInfo &qi, bool live, int pj,
                                                int64_t tj, float half_scale, unsigned char *dst, int row_p)
 {
-    const int ch = cc >> 5;
+    const int ch = cc >> 4;
     const int i0 = pos_index(qi.pos_lo[ch], pj, a.pos_lo, a.pos_hi), i1 = pos_index(qi.pos_hi[ch], pj, a.pos_lo, a.pos_hi);
     const int u0 = time_bucket(qi.ts_lo[ch], tj, a.nb), u1 = time_bucket(qi.ts_hi[ch], tj, a.nb);
     const bool one_p = __all_sync(0xffffffffu, !live || i0 == i1), one_t = __all_sync(0xffffffffu, !live || u0 == u1);
     const float bp = live ? rp[i0] : 0.f, bt = live ? rt[u0] : 0.f;
     float w = 0.f;
 #pragma unroll 1
-    for (int e8 = 0; e8 < min(n, 32); e8 += 8) {
+    for (int e8 = 0; e8 < min(n, 16); e8 += 8) {
         float x[8], b[8];
         tmem_ld8(taddr + e8, x);
 #pragma unroll
@@ -346,31 +346,19 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
 
     int2 *v_scales = reinterpret_cast<int2 *>(sm + LY::MISC + 48);  // of the tiles in the value ring, as bits
 
-    int64_t *found = reinterpret_cast<int64_t *>(sm + LY::MISC + 16);
-    const bool work = find_run(c, blockIdx.x, gridDim.x, reinterpret_cast<int64_t *>(sm + LY::P), found);
-    CacheAttnPiece *pieces = a.pieces + 2 * blockIdx.x;
-    if (threadIdx.x < 2)  // no piece, unless one is recorded at its end
-        pieces[threadIdx.x].cols = 0;
-    if (!work)
-        return;
-    Walk start;
-    start.b = (int)found[0];
-    start.left = found[2];
-    start.piece = 0;
-    start.load(c);
-    start.unit = (int)(found[1] / start.z.kt);
-    start.k = (int)(found[1] % start.z.kt);
     if (threadIdx.x == 0) {
         for (int i = 0; i < NBARS; i++) {
             int n = 1;
             if (i >= S_FULL && i < S_FULL + 4)
                 n = 2;  // S^T is there, and P^T of the item four back has been read
-            else if ((i >= P_FULL && i < P_FULL + 4) || i == Q_FULL || i == Q_FULL + 1)
+            else if ((i >= P_FULL && i < P_FULL + 4) || (i >= KEY_FULL && i < KEY_FULL + kKeySlots))
                 n = 4;
+            else if (i == Q_FULL || i == Q_FULL + 1)
+                n = 8;
             else if (i == V_FULL || i == V_FULL + 1 || (i >= C_EMPTY && i < C_EMPTY + kVStages))
                 n = D / 32;
             else if (i == Q_EMPTY || i == Q_EMPTY + 1)
-                n = 18;
+                n = 17;
             else if (i == O_FREE)
                 n = 16;
             mbar_init(bar(i), n);
@@ -384,10 +372,27 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
     }
     if (warp == 1)
         tmem_alloc(base + LY::MISC, 512);
+    int64_t *found = reinterpret_cast<int64_t *>(sm + LY::MISC + 16);
+    const bool work = find_run(c, blockIdx.x, gridDim.x, reinterpret_cast<int64_t *>(sm + LY::P), found);
+    CacheAttnPiece *pieces = a.pieces + 2 * blockIdx.x;
+    if (threadIdx.x < 2)  // no piece, unless one is recorded at its end
+        pieces[threadIdx.x].cols = 0;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(sm + LY::MISC);
+    if (!work) {
+        if (warp == 1)
+            tmem_dealloc(tmem, 512);
+        return;
+    }
+    Walk start;
+    start.b = (int)found[0];
+    start.left = found[2];
+    start.piece = 0;
+    start.load(c);
+    start.unit = (int)(found[1] / start.z.kt);
+    start.k = (int)(found[1] % start.z.kt);
     bool ok = true;
     auto wait = [&](int i, int parity) { return mbar_wait(bar(i), parity & 1, abort_flag, hdr); };
     // by a whole warp that stays converged
@@ -517,111 +522,64 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
                 }
             }
         }
-    } else if (warp == 3) {
-        // ---------------- keys' biases ----------------
-        // four keys a lane; what a tile needs is fetched ahead, one step of the chain a tile: the
-        // pages, the tokens' positions, stamps and scales, the biases
-        int g = 0;
-        for (Walk w = start; ok && w.left > 0; w.next(c)) {
-            const int qs = w.piece & 1, h = w.head(), count = w.count();
-            const float *rp = a.rab_pos + h * a.pos_hstride, *rt = a.rab_time + h * a.time_hstride;
-            struct Keys {
-                int pos[4];
-                int64_t ts[4];
-                float scale[4];  // -1: no token
-            };
-            int page[2];
-            auto pages_at = [&](int t) {
-#pragma unroll
-                for (int e = 0; e < 2; e++) {
-                    const int p = 2 * (w.k + t) + e;
-                    page[e] = t < count && p * kPage < w.s.len ? table_page(c.table, c, w.b, p) : -1;
-                }
-            };
-            auto keys_at = [&](int t, Keys &y) {
-#pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    const int r = 32 * i + lane, id = page[i >> 1];
-                    const bool live = id >= 0 && (w.k + t) * kTile + r < w.s.len;
-                    const int64_t at = live ? (int64_t)id * kPage + r % kPage : 0;
-                    y.pos[i] = c.positions[at];
-                    y.ts[i] = c.timestamps[at];
-                    y.scale[i] = live ? c.k_scale[(int64_t)id * c.H + h] : -2.f;
-                }
-            };
-            float bp[4], bt[4];
-            Keys now, next;
-            pages_at(0);
-            keys_at(0, now);
-            pages_at(1);
-            if (!(ok = wait_all(Q_FULL + qs, w.piece >> 1)))
-                break;
-            const int p_i = info[qs].pos[0];
-            const int64_t t_i = info[qs].ts[0];
-            auto biases = [&](const Keys &y) {
-#pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    bp[i] = rp[pos_index(p_i, y.pos[i], a.pos_lo, a.pos_hi)];
-                    bt[i] = rt[time_bucket(t_i, y.ts[i], a.nb)];
-                }
-            };
-            biases(now);
-            keys_at(1, next);
-            pages_at(2);
-            for (int t = 0; t < count; t++, g++) {
-                const int slot = g % kKeySlots;
-                if (g >= kKeySlots && !(ok = wait_all(KEY_EMPTY + slot, g / kKeySlots - 1)))
-                    break;
-                KeyInfo &ki = keys[slot];
-#pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    ki.bias_scale[32 * i + lane] = make_float2(0.5f * (bp[i] + bt[i]), 0.5f * now.scale[i]);
-                    ki.pos[32 * i + lane] = now.pos[i];
-                    ki.ts[32 * i + lane] = now.ts[i];
-                }
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(bar(KEY_FULL + slot));
-                biases(next);
-                now = next;
-                keys_at(t + 2, next);
-                pages_at(t + 3);
-            }
-            if (lane == 0 && ok)
-                mbar_arrive(bar(Q_EMPTY + qs));
-        }
     } else if (warp >= 20) {
-        // ---------------- queries and values ----------------
-        const int quarter = warp & 3, dim = quarter * 32 + lane;
-        // two groups of four warps: a group splits every other unit's queries and converts
-        // every other tile
-        const int group = (warp - 20) >> 2, row = threadIdx.x - 640 - 128 * group;  // of the queries
+        // ---------------- queries, keys' biases and values ----------------
+        // Two groups of four warps take every other tile each: the thread is a key of the
+        // tile first, then a dim of its values.
+        const int group = (warp - 20) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
         int g0 = 0;
         for (Walk w = start; ok && w.left > 0; w.next(c)) {
-            const int qs = w.piece & 1, h = w.head(), q0 = w.q0(), cols = w.cols();
-            if (qs == group) {
-                if (w.piece >= 2 && !(ok = wait(Q_EMPTY + qs, (w.piece >> 1) - 1)))
-                    break;
+            const int qs = w.piece & 1, h = w.head(), q0 = w.q0(), cols = w.cols(), count = w.count();
+            const float *rp = a.rab_pos + h * a.pos_hstride, *rt = a.rab_time + h * a.time_hstride;
+            // What a tile needs of a key is fetched ahead, one step of the chain a tile: its page,
+            // its position, stamp and scale (-2: no token), its biases against column 0.
+            struct Key {
+                int pos;
+                int64_t ts;
+                float scale;
+            };
+            auto page_at = [&](int t) {
+                const int j = (w.k + t) * kTile + r;
+                return t < count && j < w.s.len ? table_page(c.table, c, w.b, j / kPage) : -1;
+            };
+            auto key_at = [&](int page) {
+                const int64_t at = page >= 0 ? (int64_t)page * kPage + r % kPage : 0;
+                return Key{c.positions[at], c.timestamps[at], page >= 0 ? c.k_scale[(int64_t)page * c.H + h] : -2.f};
+            };
+            const int first = (g0 ^ group) & 1;
+            Key now = key_at(page_at(first)), next = key_at(page_at(first + 2));
+            int page = page_at(first + 4);
+            const int p_i = w.s.pos + token_pos(q0, w.s.hist, a.cand_own);
+            const int64_t t_i = c.ts[w.s.s0 + q0];
+            if (w.piece >= 2 && !(ok = wait(Q_EMPTY + qs, (w.piece >> 1) - 1)))
+                break;
+            {
+                // the queries' split: 16 rows a warp, LR lanes a row, eight elements a lane.  The
+                // row passes through the places of its two parts (eight bytes a lane in each),
+                // read back by the lane that wrote.
                 QueryInfo &qi = info[qs];
-                // LR lanes a row, eight elements a lane.  The row passes through the places of
-                // its two parts (eight bytes a lane in each), read back by the lane that wrote.
-                constexpr int LR = D / 8, RI = 32 / LR;
-                const int chunk = row >> 5, lr = lane / LR, lc = lane % LR;
+                constexpr int LR = D / 8, RI = 32 / LR, NI = 16 / RI;
+                const int chunk = warp - 20, lr = lane / LR, lc = lane % LR, row = 16 * chunk + (lane & 15);
                 const __nv_bfloat16 *qp =
                     static_cast<const __nv_bfloat16 *>(a.q) + (w.s.s0 + q0) * a.ldq + (int64_t)h * D + 8 * lc;
                 unsigned char *q1 = sm + LY::Q + 2 * qs * LY::KT;
                 auto place = [&](int rr) { return q1 + rr * D + code_chunk<D>(rr, lc >> 1) * 16 + 8 * (lc & 1); };
+                uint4 x[NI];
+#pragma unroll
+                for (int j = 0; j < NI; j++) {
+                    const int rr = 16 * chunk + RI * j + lr;
+                    x[j] = rr < cols ? *reinterpret_cast<const uint4 *>(qp + rr * a.ldq) : make_uint4(0u, 0u, 0u, 0u);
+                }
                 // positions and stamps of the chunk: their range
                 const int i = q0 + (row < cols ? row : 0);
                 const int pi = w.s.pos + token_pos(i, w.s.hist, a.cand_own);
                 const int64_t ti = c.ts[w.s.s0 + i];
-                const bool all_same = __all_sync(0xffffffffu, pi == w.s.pos + token_pos(q0, w.s.hist, a.cand_own) &&
-                                                                  ti == c.ts[w.s.s0 + q0]);
+                const bool all_same = __all_sync(0xffffffffu, pi == p_i && ti == t_i);
                 int plo = pi, phi = pi;
                 int64_t tlo = ti, thi = ti;
                 if (!all_same) {
 #pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) {
+                    for (int o = 8; o > 0; o >>= 1) {
                         plo = min(plo, __shfl_xor_sync(0xffffffffu, plo, o));
                         phi = max(phi, __shfl_xor_sync(0xffffffffu, phi, o));
                         tlo = min(tlo, __shfl_xor_sync(0xffffffffu, tlo, o));
@@ -640,31 +598,24 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
                     return m;
                 };
                 uint32_t all = 0, least = 0xffffffffu;
-#pragma unroll 1
-                for (int j0 = 0; j0 < LR; j0 += 8) {
-                    uint4 x[8];
 #pragma unroll
-                    for (int j = 0; j < 8; j++) {
-                        const int rr = 32 * chunk + RI * (j0 + j) + lr;
-                        x[j] = rr < cols ? *reinterpret_cast<const uint4 *>(qp + rr * a.ldq) : make_uint4(0u, 0u, 0u, 0u);
-                    }
-#pragma unroll
-                    for (int j = 0; j < 8; j++) {
-                        const uint32_t ww[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
-                        const uint32_t m = row_max(ww);
-                        all = max(all, m);
-                        least = min(least, m ? m : 0xffffffffu);
-                        unsigned char *at = place(32 * chunk + RI * (j0 + j) + lr);
-                        *reinterpret_cast<uint2 *>(at) = make_uint2(ww[0], ww[1]);
-                        *reinterpret_cast<uint2 *>(at + LY::KT) = make_uint2(ww[2], ww[3]);
-                    }
+                for (int j = 0; j < NI; j++) {
+                    const uint32_t ww[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+                    const uint32_t m = row_max(ww);
+                    all = max(all, m);
+                    least = min(least, m ? m : 0xffffffffu);
+                    unsigned char *at = place(16 * chunk + RI * j + lr);
+                    *reinterpret_cast<uint2 *>(at) = make_uint2(ww[0], ww[1]);
+                    *reinterpret_cast<uint2 *>(at + LY::KT) = make_uint2(ww[2], ww[3]);
                 }
                 all = __reduce_max_sync(0xffffffffu, all);
                 least = __reduce_min_sync(0xffffffffu, least);
                 // one scale for the chunk's rows if none lies far below
                 const bool one = all == 0 || (all >> 23) - (least >> 23) <= 2;
-                qi.pos[row] = pi;
-                qi.ts[row] = ti;
+                if (lane < 16) {
+                    qi.pos[row] = pi;
+                    qi.ts[row] = ti;
+                }
                 if (lane == 0) {
                     qi.chunk_scale[chunk] = one ? block_scale(all) : -1.f;
                     qi.chunk_same[chunk] = all_same;
@@ -674,8 +625,8 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
                     qi.ts_hi[chunk] = thi;
                 }
 #pragma unroll 4
-                for (int j = 0; j < LR; j++) {
-                    const int rr = 32 * chunk + RI * j + lr;
+                for (int j = 0; j < NI; j++) {
+                    const int rr = 16 * chunk + RI * j + lr;
                     unsigned char *at = place(rr);
                     const uint2 x0 = *reinterpret_cast<const uint2 *>(at);
                     const uint2 x1 = *reinterpret_cast<const uint2 *>(at + LY::KT);
@@ -700,17 +651,33 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
                 if (lane == 0)
                     mbar_arrive(bar(Q_FULL + qs));
             }
-            const int count = w.count();
-            for (int t = (g0 ^ group) & 1; dim < D && t < count; t += 2) {  // d = 64 has half the rows of V^T
-                const int g = g0 + t, k = w.k + t;
+            float bp = rp[pos_index(p_i, now.pos, a.pos_lo, a.pos_hi)], bt = rt[time_bucket(t_i, now.ts, a.nb)];
+            for (int t = first; t < count; t += 2) {
+                const int g = g0 + t, k = w.k + t, slot = g % kKeySlots;
+                if (g >= kKeySlots && !(ok = wait(KEY_EMPTY + slot, g / kKeySlots - 1)))
+                    break;
+                KeyInfo &ki = keys[slot];
+                ki.bias_scale[r] = make_float2(0.5f * (bp + bt), 0.5f * now.scale);
+                ki.pos[r] = now.pos;
+                ki.ts[r] = now.ts;
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(bar(KEY_FULL + slot));
+                now = next;
+                bp = rp[pos_index(p_i, now.pos, a.pos_lo, a.pos_hi)];
+                bt = rt[time_bucket(t_i, now.ts, a.nb)];
+                next = key_at(page);
+                page = page_at(t + 6);
+                if (r >= D)  // d = 64 has half the rows of V^T
+                    continue;
                 if (!(ok = wait(C_FULL + group, g >> 1) && (g < 2 || wait(V_EMPTY + group, (g >> 1) - 1))))
                     break;
                 const int2 sc = v_scales[group];
                 tc_fence_after();
-                const unsigned char *vrow = sm + LY::V + group * LY::KT + dim * kPage;
+                const unsigned char *vrow = sm + LY::V + group * LY::KT + r * kPage;
                 const uint32_t dst = tmem + ((uint32_t)(quarter * 32) << 16) + 384 + group * 64;
                 auto codes = [&](int i) {  // 16 keys of the tile
-                    return *reinterpret_cast<const uint4 *>(vrow + (i >> 2) * kPage * D + ((i & 3) ^ ((dim >> 1) & 3)) * 16);
+                    return *reinterpret_cast<const uint4 *>(vrow + (i >> 2) * kPage * D + ((i & 3) ^ ((r >> 1) & 3)) * 16);
                 };
                 // times the scale 2^x and the 2^120 that the conversion leaves out: one factor
                 // where bf16 has 2^(120 + x)
@@ -786,9 +753,14 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
                 a.part_w ? a.part_w + ((int64_t)((q0 + c0) / 64 * c.H + h) * c.B + w.b) * a.plan.lcap : nullptr;
             if (!(ok = wait(Q_FULL + qs, w.piece >> 1)))
                 break;
-            const int ch = c0 >> 5, ch1 = n > 32 ? ch + 1 : ch;
-            const float s0 = qi.chunk_scale[ch], s1 = qi.chunk_scale[ch1];
-            const bool same = qi.chunk_same[ch] && qi.chunk_same[ch1] && s0 != -1.f && s1 != -1.f;
+            float cs[4];  // the scales of the half's chunks
+            bool same = true;
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const int ch = (c0 >> 4) + (16 * i < n ? i : 0);
+                cs[i] = qi.chunk_scale[ch];
+                same = same && qi.chunk_same[ch] && cs[i] != -1.f;
+            }
             for (int t = first; t < count; t += step) {
                 const int it = it0 + halves * t + hf, k = w.k + t, slot = (g0 + t) % kKeySlots;
                 if (!(ok = wait(S_FULL + group, it >> 2)))
@@ -803,10 +775,10 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
                         float x[32];
                         tmem_ld32(taddr + 32 * q, x);
                         tmem_wait_ld();
-                        const float f = bs.y * (q ? s1 : s0);
+                        const float f0 = bs.y * (q ? cs[2] : cs[0]), f1 = bs.y * (q ? cs[3] : cs[1]);
 #pragma unroll
                         for (int e = 0; e < 32; e++)
-                            x[e] = silu_half(fmaf(x[e], f, bs.x));
+                            x[e] = silu_half(fmaf(x[e], e < 16 ? f0 : f1, bs.x));
 #pragma unroll
                         for (int e = 0; e < 4; e++)
                             put_p8(x + 8 * e, prow + ((4 * q + e) ^ (row_p & 7)) * 16);
@@ -827,7 +799,7 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
                 } else {
                     const int pj = keys[slot].pos[r];
                     const int64_t tj = keys[slot].ts[r];
-                    for (int cc = 0; cc < n; cc += 32)
+                    for (int cc = 0; cc < n; cc += 16)
                         wsum += chunk_general(taddr + cc, c0 + cc, n - cc, a, rp, rt, qi, live, pj, tj, bs.y, prow, row_p);
                 }
                 if (!live)  // no token, and S^T of whatever the tile holds there: P is 0
