@@ -67,8 +67,13 @@ struct KeyInfo {
     int64_t ts[kTile];
 };
 
-// what the epilogue needs to know of a unit's queries
+// A piece of the run, and what the epilogue needs to know of its queries.  Written by the
+// warps that split the queries; the MMA and epilogue warps know the run from here alone.
 struct QueryInfo {
+    int64_t row;    // first row
+    int64_t plane;  // of part_w: the first 64 queries' weights of the piece's first key
+    int count, cols;  // tiles (0: the run has ended), queries
+    int head, k, whole, last;  // first tile; the whole unit; up to the unit's end
     float chunk_scale[8];  // one scale of 16 columns, or -1: each its own
     int chunk_same[8];     // every column has row 0's position and stamp
     int pos_lo[8], pos_hi[8];  // a chunk's least and largest position and stamp
@@ -284,11 +289,12 @@ __device__ __forceinline__ void put_p8(const float *x, unsigned char *dst)
 // A chunk of 16 queries whose biases or scales differ: this key's P^T, and the sum of
 // its magnitudes over the first n.  Where the whole warp's pairs share an index of a
 // table, it is read once.  Eight queries at a time: the common loop keeps its registers.
-__device__ __forceinline__ float chunk_general(uint32_t taddr, int cc, int n, const CacheAttnArgs &a, const float *rp,
-                                               const float *rt, const QueryInfo &qi, bool live, int pj,
+__device__ __forceinline__ float chunk_general(uint32_t taddr, int cc, int n, const CacheAttnArgs &a,
+                                               const QueryInfo &qi, bool live, int pj,
                                                int64_t tj, float half_scale, unsigned char *dst, int row_p)
 {
     const int ch = cc >> 4;
+    const float *rp = a.rab_pos + qi.head * a.pos_hstride, *rt = a.rab_time + qi.head * a.time_hstride;
     const int i0 = pos_index(qi.pos_lo[ch], pj, a.pos_lo, a.pos_hi), i1 = pos_index(qi.pos_hi[ch], pj, a.pos_lo, a.pos_hi);
     const int u0 = time_bucket(qi.ts_lo[ch], tj, a.nb), u1 = time_bucket(qi.ts_hi[ch], tj, a.nb);
     const bool one_p = __all_sync(0xffffffffu, !live || i0 == i1), one_t = __all_sync(0xffffffffu, !live || u0 == u1);
@@ -358,7 +364,7 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
             else if (i == V_FULL || i == V_FULL + 1 || (i >= C_EMPTY && i < C_EMPTY + kVStages))
                 n = D / 32;
             else if (i == Q_EMPTY || i == Q_EMPTY + 1)
-                n = 17;
+                n = 18;
             else if (i == O_FREE)
                 n = 16;
             mbar_init(bar(i), n);
@@ -449,9 +455,12 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
     } else if (warp == 1) {
         // ---------------- S^T = K Q^T ----------------
         int g = 0, it = 0;
-        for (Walk w = start; ok && w.left > 0; w.next(c)) {
-            const int qs = w.piece & 1, count = w.count(), halves = w.cols() > 64 ? 2 : 1;
-            if (!(ok = wait_all(Q_FULL + qs, w.piece >> 1)))
+        for (int piece = 0; ok; piece++) {
+            const int qs = piece & 1;
+            if (!(ok = wait_all(Q_FULL + qs, piece >> 1)))
+                break;
+            const int count = info[qs].count, halves = info[qs].cols > 64 ? 2 : 1;
+            if (count == 0)
                 break;
             for (int t = 0; ok && t < count; t++, g++) {
                 const int st = g % kKStages;
@@ -491,9 +500,17 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
     } else if (warp == 2) {
         // ---------------- O^T += V^T P^T ----------------
         int g = 0, it = 0;
-        for (Walk w = start; ok && w.left > 0; w.next(c)) {
-            const int count = w.count(), halves = w.cols() > 64 ? 2 : 1;
-            if (w.piece > 0 && !(ok = wait_all(O_FREE, w.piece - 1)))
+        for (int piece = 0; ok; piece++) {
+            const int qs = piece & 1;
+            if (!(ok = wait_all(Q_FULL + qs, piece >> 1)))
+                break;
+            const int count = info[qs].count, halves = info[qs].cols > 64 ? 2 : 1;
+            if (count == 0)
+                break;
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(bar(Q_EMPTY + qs));
+            if (piece > 0 && !(ok = wait_all(O_FREE, piece - 1)))
                 break;
             for (int t = 0; ok && t < count; t++, g++) {
                 const int vb = g & 1;
@@ -527,7 +544,7 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
         // Two groups of four warps take every other tile each: the thread is a key of the
         // tile first, then a dim of its values.
         const int group = (warp - 20) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
-        int g0 = 0;
+        int g0 = 0, pieces_done = 0;
         for (Walk w = start; ok && w.left > 0; w.next(c)) {
             const int qs = w.piece & 1, h = w.head(), q0 = w.q0(), cols = w.cols(), count = w.count();
             const float *rp = a.rab_pos + h * a.pos_hstride, *rt = a.rab_time + h * a.time_hstride;
@@ -615,6 +632,16 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
                 if (lane < 16) {
                     qi.pos[row] = pi;
                     qi.ts[row] = ti;
+                }
+                if (chunk == 0 && lane == 0) {
+                    qi.row = w.s.s0 + q0;
+                    qi.plane = ((int64_t)(q0 / 64 * c.H + h) * c.B + w.b) * a.plan.lcap + (int64_t)w.k * kTile;
+                    qi.count = count;
+                    qi.cols = cols;
+                    qi.head = h;
+                    qi.k = w.k;
+                    qi.whole = w.k == 0 && count == w.z.kt;
+                    qi.last = w.k + count == w.z.kt;
                 }
                 if (lane == 0) {
                     qi.chunk_scale[chunk] = one ? block_scale(all) : -1.f;
@@ -732,6 +759,15 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
                 }
             }
             g0 += count;
+            pieces_done++;
+        }
+        const int qs = pieces_done & 1;
+        if (ok && (pieces_done < 2 || wait(Q_EMPTY + qs, (pieces_done >> 1) - 1))) {
+            if (warp == 20 && lane == 0)
+                info[qs].count = 0;
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(bar(Q_FULL + qs));
         }
     } else if (warp >= 4) {
         // ---------------- S^T to P^T ----------------
@@ -740,29 +776,26 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
         const uint32_t trow = tmem + ((uint32_t)(quarter * 32) << 16), taddr = trow + group * 64;
         unsigned char *prow = sm + LY::P + group * kPanel + row_p * 128;
         int it0 = 0, g0 = 0;  // items and tiles before this piece
-        for (Walk w = start; ok && w.left > 0; w.next(c)) {
-            const int qs = w.piece & 1, h = w.head(), q0 = w.q0(), cols = w.cols(), count = w.count();
-            const float *rp = a.rab_pos + h * a.pos_hstride, *rt = a.rab_time + h * a.time_hstride;
+        for (int piece = 0; ok; piece++) {
+            const int qs = piece & 1;
             const QueryInfo &qi = info[qs];
+            if (!(ok = wait(Q_FULL + qs, piece >> 1)))
+                break;
+            const int count = qi.count;
+            if (count == 0)
+                break;
             // Items (a tile's 64 columns) go round the groups; a group keeps its buffer, and
             // within a unit its half.
-            const int halves = cols > 64 ? 2 : 1, i0 = (group - it0) & 3;  // the group's first item here
+            const int halves = qi.cols > 64 ? 2 : 1, i0 = (group - it0) & 3;  // the group's first item here
             const int hf = halves == 2 ? i0 & 1 : 0, first = halves == 2 ? i0 >> 1 : i0, step = 4 / halves;
-            const int c0 = hf * 64, n = min(cols - c0, 64);
-            float *plane =
-                a.part_w ? a.part_w + ((int64_t)((q0 + c0) / 64 * c.H + h) * c.B + w.b) * a.plan.lcap : nullptr;
-            if (!(ok = wait(Q_FULL + qs, w.piece >> 1)))
-                break;
-            float cs[4];  // the scales of the half's chunks
+            const int c0 = hf * 64, n = min(qi.cols - c0, 64);
+            const float *cs = qi.chunk_scale + 4 * hf;  // the scales of the half's chunks
             bool same = true;
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const int ch = (c0 >> 4) + (16 * i < n ? i : 0);
-                cs[i] = qi.chunk_scale[ch];
-                same = same && qi.chunk_same[ch] && cs[i] != -1.f;
-            }
+            for (int i = 0; i < 4; i++)
+                same = same && (16 * i >= n || (qi.chunk_same[4 * hf + i] && cs[i] != -1.f));
             for (int t = first; t < count; t += step) {
-                const int it = it0 + halves * t + hf, k = w.k + t, slot = (g0 + t) % kKeySlots;
+                const int it = it0 + halves * t + hf, slot = (g0 + t) % kKeySlots;
                 if (!(ok = wait(S_FULL + group, it >> 2)))
                     break;
                 tc_fence_after();
@@ -775,14 +808,14 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
                         float x[32];
                         tmem_ld32(taddr + 32 * q, x);
                         tmem_wait_ld();
-                        const float f0 = bs.y * (q ? cs[2] : cs[0]), f1 = bs.y * (q ? cs[3] : cs[1]);
+                        const float f0 = bs.y * cs[2 * q], f1 = bs.y * cs[2 * q + 1];
 #pragma unroll
                         for (int e = 0; e < 32; e++)
                             x[e] = silu_half(fmaf(x[e], e < 16 ? f0 : f1, bs.x));
 #pragma unroll
                         for (int e = 0; e < 4; e++)
                             put_p8(x + 8 * e, prow + ((4 * q + e) ^ (row_p & 7)) * 16);
-                        if (plane) {
+                        if (a.part_w) {
                             float w0 = 0.f, w1 = 0.f;
                             if (n >= 32 * q + 32) {
 #pragma unroll
@@ -800,7 +833,7 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
                     const int pj = keys[slot].pos[r];
                     const int64_t tj = keys[slot].ts[r];
                     for (int cc = 0; cc < n; cc += 16)
-                        wsum += chunk_general(taddr + cc, c0 + cc, n - cc, a, rp, rt, qi, live, pj, tj, bs.y, prow, row_p);
+                        wsum += chunk_general(taddr + cc, c0 + cc, n - cc, a, qi, live, pj, tj, bs.y, prow, row_p);
                 }
                 if (!live)  // no token, and S^T of whatever the tile holds there: P is 0
                     for (int e = 0; e < 8; e++)
@@ -810,15 +843,15 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(bar(P_FULL + group));
-                if (plane && k * kTile + r < a.plan.lcap)
-                    plane[k * kTile + r] = live ? wsum : 0.f;
+                if (a.part_w && (qi.k + t) * kTile + r < a.plan.lcap)
+                    a.part_w[qi.plane + (int64_t)hf * c.H * c.B * a.plan.lcap + t * kTile + r] = live ? wsum : 0.f;
             }
             g0 += count;
             it0 += count * halves;
-            const bool whole = w.k == 0 && count == w.z.kt;
+            const bool whole = qi.whole;
             // this group's quarter of the columns; the addend of a whole unit, before the wait
-            const int col0 = group * 32, nc = min(cols - col0, 32);
-            const int64_t at = ((w.s.s0 + q0 + col0 + (lane >> 2)) * c.H + h) * D + quarter * 32 + 8 * (lane & 3);
+            const int col0 = group * 32, nc = min(qi.cols - col0, 32);
+            const int64_t at = ((qi.row + col0 + (lane >> 2)) * c.H + qi.head) * D + quarter * 32 + 8 * (lane & 3);
             const int64_t eight = (int64_t)8 * c.H * D;  // eight queries on
             uint4 add[4];
             if (whole && a.addend && quarter * 32 < D)
@@ -826,12 +859,12 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
                 for (int i = 0; i < 4; i++)
                     if (8 * i + (lane >> 2) < nc)
                         add[i] = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.addend) + at + i * eight);
-            if (!(ok = ok && wait(O_FULL, w.piece)))
+            if (!(ok = ok && wait(O_FULL, piece)))
                 break;
             tc_fence_after();
             // O^T: lane = dim, column = query.  A whole unit leaves through the warp's own rows of
             // its P^T buffer, 32 queries x 32 dims, so that memory sees 16-byte accesses.
-            const int slot = w.k > 0 ? 0 : 1;
+            const int slot = qi.k > 0 ? 0 : 1;
             if (quarter * 32 < D && nc > 0) {
                 unsigned char *stage = sm + LY::P + group * kPanel + quarter * 4096;
                 float ov[32];
@@ -873,19 +906,13 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
                     __syncwarp();
                 }
             }
+            if (!whole && warp == 4 && lane == 0)
+                pieces[slot] = CacheAttnPiece{qi.row, qi.head, qi.cols, qi.last};
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(bar(O_FREE));
                 mbar_arrive(bar(Q_EMPTY + qs));
-            }
-            if (!whole && warp == 4 && lane == 0) {
-                CacheAttnPiece p;
-                p.row = w.s.s0 + q0;
-                p.head = h;
-                p.cols = cols;
-                p.last = w.k + count == w.z.kt;
-                pieces[slot] = p;
             }
         }
     }
