@@ -270,12 +270,12 @@ __device__ __forceinline__ bool elect_one()
     return p != 0;
 }
 
-// 32 lanes x 8 consecutive 32-bit columns
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float *v)
+// 32 lanes x 4 consecutive 32-bit columns
+__device__ __forceinline__ void tmem_ld4(uint32_t taddr, float *v)
 {
     uint32_t *r = reinterpret_cast<uint32_t *>(v);
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(taddr));
 }
 
@@ -288,7 +288,7 @@ __device__ __forceinline__ void put_p8(const float *x, unsigned char *dst)
 
 // A chunk of 16 queries whose biases or scales differ: this key's P^T, and the sum of
 // its magnitudes over the first n.  Where the whole warp's pairs share an index of a
-// table, it is read once.  Eight queries at a time: the common loop keeps its registers.
+// table, it is read once.
 __device__ __forceinline__ float chunk_general(uint32_t taddr, int cc, int n, const CacheAttnArgs &a,
                                                const QueryInfo &qi, bool live, int pj,
                                                int64_t tj, float half_scale, unsigned char *dst, int row_p)
@@ -300,34 +300,25 @@ __device__ __forceinline__ float chunk_general(uint32_t taddr, int cc, int n, co
     const bool one_p = __all_sync(0xffffffffu, !live || i0 == i1), one_t = __all_sync(0xffffffffu, !live || u0 == u1);
     const float bp = live ? rp[i0] : 0.f, bt = live ? rt[u0] : 0.f;
     float w = 0.f;
+    // rolled: short runs pay for every line of code they fetch for the first time
 #pragma unroll 1
-    for (int e8 = 0; e8 < min(n, 16); e8 += 8) {
-        float x[8], b[8];
-        tmem_ld8(taddr + e8, x);
+    for (int e0 = 0; e0 < 16; e0 += 4) {
+        float x[4], b[4];
+        tmem_ld4(taddr + e0, x);
 #pragma unroll
-        for (int e = 0; e < 8; e++)
-            b[e] = bp;
-        if (!one_p && live)
+        for (int e = 0; e < 4; e++)
+            b[e] = one_p ? bp : rp[pos_index(qi.pos[cc + e0 + e], pj, a.pos_lo, a.pos_hi)];
 #pragma unroll
-            for (int e = 0; e < 8; e++)
-                b[e] = rp[pos_index(qi.pos[cc + e8 + e], pj, a.pos_lo, a.pos_hi)];
-        if (one_t) {
-#pragma unroll
-            for (int e = 0; e < 8; e++)
-                b[e] += bt;
-        } else if (live) {
-#pragma unroll
-            for (int e = 0; e < 8; e++)
-                b[e] += rt[time_bucket(qi.ts[cc + e8 + e], tj, a.nb)];
-        }
-        __syncwarp();
+        for (int e = 0; e < 4; e++)
+            b[e] += one_t ? bt : rt[time_bucket(qi.ts[cc + e0 + e], tj, a.nb)];
         tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 8; e++) {
-            x[e] = silu_half(fmaf(x[e], half_scale * qi.scale[cc + e8 + e], 0.5f * b[e]));
-            w += e8 + e < n ? fabsf(x[e]) : 0.f;
+        for (int e = 0; e < 4; e++) {
+            x[e] = silu_half(fmaf(x[e], half_scale * qi.scale[cc + e0 + e], 0.5f * b[e]));
+            w += e0 + e < n ? fabsf(x[e]) : 0.f;
         }
-        put_p8(x, dst + ((((cc + e8) >> 3 & 7) ^ (row_p & 7)) * 16));
+        *reinterpret_cast<uint2 *>(dst + ((((cc + e0) >> 3 & 7) ^ (row_p & 7)) * 16) + 2 * (e0 & 4)) =
+            make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
     }
     return w;
 }
@@ -397,8 +388,13 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
     start.left = found[2];
     start.piece = 0;
     start.load(c);
-    start.unit = (int)(found[1] / start.z.kt);
-    start.k = (int)(found[1] % start.z.kt);
+    if (found[1] >> 31) {
+        start.unit = (int)(found[1] / start.z.kt);
+        start.k = (int)(found[1] % start.z.kt);
+    } else {
+        start.unit = (int)found[1] / start.z.kt;
+        start.k = (int)found[1] % start.z.kt;
+    }
     bool ok = true;
     auto wait = [&](int i, int parity) { return mbar_wait(bar(i), parity & 1, abort_flag, hdr); };
     // by a whole warp that stays converged
@@ -563,11 +559,12 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
                 const int64_t at = page >= 0 ? (int64_t)page * kPage + r % kPage : 0;
                 return Key{c.positions[at], c.timestamps[at], page >= 0 ? c.k_scale[(int64_t)page * c.H + h] : -2.f};
             };
-            const int first = (g0 ^ group) & 1;
-            Key now = key_at(page_at(first)), next = key_at(page_at(first + 2));
+            const int first = (g0 ^ group) & 1, page0 = page_at(first), page1 = page_at(first + 2);
             int page = page_at(first + 4);
             const int p_i = w.s.pos + token_pos(q0, w.s.hist, a.cand_own);
             const int64_t t_i = c.ts[w.s.s0 + q0];
+            Key now, next;
+            float bp, bt;
             if (w.piece >= 2 && !(ok = wait(Q_EMPTY + qs, (w.piece >> 1) - 1)))
                 break;
             {
@@ -587,6 +584,8 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
                     const int rr = 16 * chunk + RI * j + lr;
                     x[j] = rr < cols ? *reinterpret_cast<const uint4 *>(qp + rr * a.ldq) : make_uint4(0u, 0u, 0u, 0u);
                 }
+                now = key_at(page0);
+                next = key_at(page1);
                 // positions and stamps of the chunk: their range
                 const int i = q0 + (row < cols ? row : 0);
                 const int pi = w.s.pos + token_pos(i, w.s.hist, a.cand_own);
@@ -627,6 +626,8 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
                 }
                 all = __reduce_max_sync(0xffffffffu, all);
                 least = __reduce_min_sync(0xffffffffu, least);
+                bp = rp[pos_index(p_i, now.pos, a.pos_lo, a.pos_hi)];
+                bt = rt[time_bucket(t_i, now.ts, a.nb)];
                 // one scale for the chunk's rows if none lies far below
                 const bool one = all == 0 || (all >> 23) - (least >> 23) <= 2;
                 if (lane < 16) {
@@ -678,7 +679,6 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
                 if (lane == 0)
                     mbar_arrive(bar(Q_FULL + qs));
             }
-            float bp = rp[pos_index(p_i, now.pos, a.pos_lo, a.pos_hi)], bt = rt[time_bucket(t_i, now.ts, a.nb)];
             for (int t = first; t < count; t += 2) {
                 const int g = g0 + t, k = w.k + t, slot = g % kKeySlots;
                 if (g >= kKeySlots && !(ok = wait(KEY_EMPTY + slot, g / kKeySlots - 1)))
