@@ -74,15 +74,17 @@ cache_attn_rows_kernel(const CacheAttnArgs a)
     int x = blockIdx.x;
     const int h = x % c.H;
     x /= c.H;
+    const int tile = x % a.plan.qtiles;  // of R query rows
+    x /= a.plan.qtiles;
     const int part = x % a.plan.nsplit, b = x / a.plan.nsplit;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const CacheSeq s = cache_seq(c, b);
-    const int rows = s.n;  // at most R: the launch is chosen by max_seq_len
+    const int r0 = tile * R, rows = min(s.n - r0, R);
     const int p0 = part * a.plan.split_pages, p1 = min((s.len + kPage - 1) / kPage, p0 + a.plan.split_pages);
-    if (rows == 0 || p0 >= p1)
+    if (rows <= 0 || p0 >= p1)
         return;
     float *bias = smem + warp * R * kBiasLd;
-    float *wplane = a.part_w ? a.part_w + ((int64_t)h * c.B + b) * a.plan.lcap : nullptr;
+    float *wplane = a.part_w ? a.part_w + ((int64_t)(tile * c.H + h) * c.B + b) * a.plan.lcap : nullptr;
 
     uint4 kr[KN * NC], vr[VN];
     auto load_k = [&](int page) {
@@ -103,7 +105,7 @@ cache_attn_rows_kernel(const CacheAttnArgs a)
         if (p >= p1)
             return -1;
         const int page = table_page(c.table, c, b, p);
-        if (page < 0 && h == 0 && lane == 0)
+        if (page < 0 && h == 0 && tile == 0 && lane == 0)
             atomicOr(&c.hdr->flag, FLAG_CACHE_PAGE);
         return page;
     };
@@ -114,7 +116,7 @@ cache_attn_rows_kernel(const CacheAttnArgs a)
         load_v(page);
     }
     if (threadIdx.x < R) {
-        const int i = min((int)threadIdx.x, rows - 1);
+        const int i = r0 + min((int)threadIdx.x, rows - 1);
         row_pi[threadIdx.x] = s.pos + token_pos(i, s.hist, a.cand_own);
         row_ti[threadIdx.x] = c.ts[s.s0 + i];
     }
@@ -125,7 +127,7 @@ cache_attn_rows_kernel(const CacheAttnArgs a)
     for (int rt = 0; rt < RT; rt++) {
         const bool live = g + 8 * rt < rows;
         const __nv_bfloat16 *qp =
-            static_cast<const __nv_bfloat16 *>(a.q) + (s.s0 + (live ? g + 8 * rt : 0)) * a.ldq + (int64_t)h * D + 16 * t;
+            static_cast<const __nv_bfloat16 *>(a.q) + (s.s0 + r0 + (live ? g + 8 * rt : 0)) * a.ldq + (int64_t)h * D + 16 * t;
         uint32_t w[8 * NC];
         float m = 0.f;
 #pragma unroll
@@ -293,7 +295,7 @@ cache_attn_rows_kernel(const CacheAttnArgs a)
 #pragma unroll
         for (int w = 0; w < kWarps; w++)
             sum += smem[w * R * D + i];
-        a.part_o[(((int64_t)part * c.T + s.s0 + i / D) * c.H + h) * D + i % D] = sum;
+        a.part_o[(((int64_t)part * c.T + s.s0 + r0 + i / D) * c.H + h) * D + i % D] = sum;
     }
 }
 
@@ -302,7 +304,7 @@ cudaError_t rows_launch(const CacheAttnArgs &a, cudaStream_t stream)
 {
     constexpr int bytes = kWarps * 8 * RT * std::max(D, kBiasLd) * 4;
     static_assert(bytes <= 48 * 1024, "within the default dynamic shared memory");
-    const int64_t grid = (int64_t)a.c.B * a.plan.nsplit * a.c.H;
+    const int64_t grid = (int64_t)a.c.B * a.plan.nsplit * a.plan.qtiles * a.c.H;
     cache_attn_rows_kernel<D, RT><<<(unsigned)grid, kWarps * 32, bytes, stream>>>(a);
     return cudaGetLastError();
 }

@@ -182,7 +182,7 @@ cudaError_t launch_cache_evict(const CacheCall &c, int keep, int first, int rece
 // with two slots [128, d] of part_o and two piece records each.  Where weights are
 // taken, those of plane_rows queries and one head go to a plane of part_w [planes, B, lcap].  A second
 // kernel joins them in a fixed order.
-constexpr int kCacheRows = 16;
+constexpr int kCacheRows = 64;
 enum CacheKernel { CACHE_F32, CACHE_ROWS, CACHE_TC };
 struct CacheAttnPlan {
     CacheKernel kernel;
