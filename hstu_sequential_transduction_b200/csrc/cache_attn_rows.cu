@@ -2,33 +2,37 @@
 //
 //   O_i = inv_n sum_j SiLU(q_i . k_j + bias_ij) v_j,   a_j += |inv_n| sum_ih |SiLU|
 //
-// Bound by HBM: the codes of a page (64 d bytes of keys, as many of values per head)
-// are read once for all rows, straight into the registers of one warp, with no
-// staging and no shuffles: a page's layouts (keys [64][d], values [d][64]) are the
-// column-major B operands of the 16-bit matrix instructions, and the order of the
-// contracted index is free, so a lane's 16-byte load is four instructions' operand:
-//   S = Q K^T: lane (g, t) = (lane / 4, lane % 4) loads bytes [64 c + 16 t, + 16) of
-//   key row 16 (g / 2) + 2 n + g % 2 for tile n; dims 4 u .. 4 u + 3 of that load
-//   serve step (c, u).  The result then holds row g, keys 16 t + 2 n, + 1;
-//   O = P V: which is the A operand for keys 16 t + 4 s .. + 3 of step s, word s of
-//   the 16-byte load at keys 16 t of value row (dim) 8 n + g.
+// Bound by HBM: the codes of a page (64 d bytes of keys, as many of values per head) are
+// read once for all rows.  A warp has a buffer for one block of keys and one of values,
+// filled by bulk copies: while the values are used the next keys are on their way, and
+// the other way round; three CTAs of four warps keep some 100 KB an SM in flight.
+// (Loaded straight into registers, the blocks left two warps a scheduler: 4.1 TB/s.)
+// Keys and dims are the rows of the 16-bit matrix instructions, the queries their eight
+// columns, so that a page of d = 128 takes 64 of them for eight queries (with queries as
+// the sixteen rows it took 128, and those were the bound: 200 us where this takes 1XX).
+//   S^T = K Q^T, O^T = V^T P^T
+// A page's layouts (keys [64][d], values [d][64]) are row-major A operands, and the order
+// of the contracted index is free, so a lane's 16-byte read is four instructions' operand:
+// lane (g, t) = (lane / 4, lane % 4) reads bytes [64 c + 16 t, + 16) of the key rows
+// 16 (g / 2) + 4 m + g % 2 and + 2 for tile m, and bytes [16 t, + 16) (keys) of value rows
+// 16 n + g and + 8.  Tile m of S^T then holds, after an 8 x 8 transposition in the warp,
+// the B operand for word m of the values.
 // Codes become f16 exactly.  q becomes f16 under a power of two per row that puts
 // its largest magnitude into [2^14, 2^15): exact but for elements below 2^-28 of it.
 // P becomes f16 under a power of two per page and row, of its largest magnitude, so
 // its one rounding is 2^-11 of each value down to 2^-28 of the page's largest; each
 // page's product starts from zero and is added to the float32 sums with the page's
-// scale.  Legacy matrix instructions are enough: a page takes 128 of them per 16 KB.
+// scale.
 #include <algorithm>
 
 #include "cache.cuh"
+#include "tc_common.cuh"
 
 namespace hstu {
 
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kBiasLd = 68;  // floats of a row of staged biases
-
 __device__ __forceinline__ void mma_f16(float *d, const uint32_t *a, uint32_t b0, uint32_t b1)
 {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
@@ -42,6 +46,14 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
+// 8 x 8 transposition in the warp: lane (g, t) gives row g, columns 2 t, + 1
+__device__ __forceinline__ uint32_t transpose8(uint32_t x)
+{
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
+    return y;
+}
+
 // 2^(14 - e) for a magnitude with exponent e (at least -100), and its inverse
 __device__ __forceinline__ float to_range(float m, float *inverse)
 {
@@ -50,26 +62,28 @@ __device__ __forceinline__ float to_range(float m, float *inverse)
     return __int_as_float((268 - e) << 23);
 }
 
-__device__ __forceinline__ uint4 ldg_stream(const uint8_t *p)
+// untiled copy of `bytes` (a multiple of 16) to shared memory
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
 {
-    uint4 w;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n"
-                 : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
-                 : "l"(p));
-    return w;
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
 }
 
 __device__ __forceinline__ uint32_t word(const uint4 &w, int i) { return i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w; }
 
 // RT: row tiles of 8 (1 or 2)
 template <int D, int RT>
-__global__ void __launch_bounds__(kWarps * 32, RT == 1 ? 2 : 1)
+__global__ void __launch_bounds__(kWarps * 32, RT == 1 ? 3 : 2)
 cache_attn_rows_kernel(const CacheAttnArgs a)
 {
-    constexpr int R = 8 * RT, NC = D / 64, KN = 8, VN = D / 8;
-    extern __shared__ __align__(16) float smem[];
+    constexpr int R = 8 * RT, NC = D / 64, VN = D / 16, kBiasLd = R + 2;
+    constexpr int kBlock = kPage * D;
+    extern __shared__ __align__(16) unsigned char smem[];  // blocks of keys and values per warp, biases
     __shared__ int row_pi[R];
     __shared__ int64_t row_ti[R];
+    __shared__ __align__(8) uint64_t bars[kWarps][2];
+    __shared__ volatile int abort_flag;
     const CacheCall &c = a.c;
     int x = blockIdx.x;
     const int h = x % c.H;
@@ -83,23 +97,25 @@ cache_attn_rows_kernel(const CacheAttnArgs a)
     const int p0 = part * a.plan.split_pages, p1 = min((s.len + kPage - 1) / kPage, p0 + a.plan.split_pages);
     if (rows <= 0 || p0 >= p1)
         return;
-    float *bias = smem + warp * R * kBiasLd;
+    float *bias = reinterpret_cast<float *>(smem + kWarps * 2 * kBlock) + warp * kPage * kBiasLd;
     float *wplane = a.part_w ? a.part_w + ((int64_t)(tile * c.H + h) * c.B + b) * a.plan.lcap : nullptr;
-
-    uint4 kr[KN * NC], vr[VN];
-    auto load_k = [&](int page) {
-        const uint8_t *kc = c.k_codes + block_offset<D>(page, c.H, h) + (16 * (g >> 1) + (g & 1)) * D + 16 * t;
-#pragma unroll
-        for (int n = 0; n < KN; n++)
-#pragma unroll
-            for (int cc = 0; cc < NC; cc++)
-                kr[n * NC + cc] = ldg_stream(kc + 2 * n * D + 64 * cc);
-    };
-    auto load_v = [&](int page) {
-        const uint8_t *vc = c.v_codes + block_offset<D>(page, c.H, h) + g * kPage + 16 * t;
-#pragma unroll
-        for (int n = 0; n < VN; n++)
-            vr[n] = ldg_stream(vc + n * 8 * kPage);
+    const unsigned char *kbuf = smem + warp * 2 * kBlock, *vbuf = kbuf + kBlock;
+    const uint32_t kbar = smem_u32(&bars[warp][0]), vbar = smem_u32(&bars[warp][1]);
+    if (lane == 0) {
+        mbar_init(kbar, 1);
+        mbar_init(vbar, 1);
+        if (warp == 0)
+            abort_flag = 0;
+        fence_mbar_init();
+    }
+    __syncwarp();
+    // by one lane, once the warp is done with what the buffer held
+    auto load = [&](const uint8_t *codes, const unsigned char *buf, uint32_t bar, int page) {
+        __syncwarp();
+        if (lane == 0) {
+            mbar_expect_tx(bar, kBlock);
+            bulk_load(smem_u32(buf), codes + block_offset<D>(page, c.H, h), kBlock, bar);
+        }
     };
     auto page_of = [&](int p) {
         if (p >= p1)
@@ -112,8 +128,8 @@ cache_attn_rows_kernel(const CacheAttnArgs a)
     int p = p0 + warp;
     int page = page_of(p);
     if (page >= 0) {
-        load_k(page);
-        load_v(page);
+        load(c.k_codes, kbuf, kbar, page);
+        load(c.v_codes, vbuf, vbar, page);
     }
     if (threadIdx.x < R) {
         const int i = r0 + min((int)threadIdx.x, rows - 1);
@@ -122,7 +138,7 @@ cache_attn_rows_kernel(const CacheAttnArgs a)
     }
     // q: for step (cc, u), dims 64 cc + 16 t + 4 u .. + 3 of rows g and g + 8
     uint32_t qf[4 * NC][2 * RT];
-    float qinv[RT];
+    float qinv[RT][2];  // of queries 8 rt + 2 t, + 1
 #pragma unroll
     for (int rt = 0; rt < RT; rt++) {
         const bool live = g + 8 * rt < rows;
@@ -142,20 +158,28 @@ cache_attn_rows_kernel(const CacheAttnArgs a)
             m = fmaxf(m, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xffff0000u))));
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        const float f = to_range(m, &qinv[rt]);
+        float inv;
+        const float f = to_range(m, &inv);
+#pragma unroll
+        for (int e = 0; e < 2; e++)
+            qinv[rt][e] = __shfl_sync(0xffffffffu, inv, 4 * (2 * t + e));
 #pragma unroll
         for (int e = 0; e < 8 * NC; e++)  // word e: dims 2 e, 2 e + 1 of the lane's 16 NC
-            qf[e >> 1][rt + RT * (e & 1)] =
+            qf[e >> 1][2 * rt + (e & 1)] =
                 pack_f16(__uint_as_float(w[e] << 16) * f, __uint_as_float(w[e] & 0xffff0000u) * f);
     }
-    float o[VN][2 * RT];
+    float o[RT][VN][4];  // dims 16 n + g (+ 8), queries 8 rt + 2 t, + 1
 #pragma unroll
-    for (int n = 0; n < VN; n++)
+    for (int rt = 0; rt < RT; rt++)
 #pragma unroll
-        for (int e = 0; e < 2 * RT; e++)
-            o[n][e] = 0.f;
+        for (int n = 0; n < VN; n++)
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+                o[rt][n][e] = 0.f;
     const float *rp = a.rab_pos + h * a.pos_hstride, *rt_ = a.rab_time + h * a.time_hstride;
     __syncthreads();
+    bool ok = true;
+    uint32_t loads = 0;  // blocks of each kind used so far
     for (; p < p1; p += kWarps) {
         const int count = min(s.len - p * kPage, kPage);
         const int next = page_of(p + kWarps);
@@ -165,8 +189,8 @@ cache_attn_rows_kernel(const CacheAttnArgs a)
                     wplane[p * kPage + j] = 0.f;
             page = next;
             if (page >= 0) {
-                load_k(page);
-                load_v(page);
+                load(c.k_codes, kbuf, kbar, page);
+                load(c.v_codes, vbuf, vbar, page);
             }
             continue;
         }
@@ -179,122 +203,145 @@ cache_attn_rows_kernel(const CacheAttnArgs a)
             const int pj = c.positions[at];
             const int64_t tj = c.timestamps[at];
             for (int r = 0; r < rows; r++)
-                bias[r * kBiasLd + lane + 32 * e] =
+                bias[(lane + 32 * e) * kBiasLd + r] =
                     rp[pos_index(row_pi[r], pj, a.pos_lo, a.pos_hi)] + rt_[time_bucket(row_ti[r], tj, a.nb)];
         }
         __syncwarp();
-        float sc[KN][4];
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(kbar, loads & 1, &abort_flag, c.hdr))))
+            break;
+        float sc[RT][4][4];  // keys of tile m: 16 (g / 2) + 4 m + g % 2 (+ 2), queries 2 t, + 1
+        const int key0 = 16 * (g >> 1) + (g & 1);
+        const unsigned char *krow = kbuf + key0 * D + 16 * t;
 #pragma unroll
-        for (int n = 0; n < KN; n++) {
-            sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
+        for (int m = 0; m < 4; m++) {
+            uint4 ka[NC], kb[NC];
+#pragma unroll
+            for (int cc = 0; cc < NC; cc++) {
+                ka[cc] = *reinterpret_cast<const uint4 *>(krow + 4 * m * D + 64 * cc);
+                kb[cc] = *reinterpret_cast<const uint4 *>(krow + (4 * m + 2) * D + 64 * cc);
+            }
+#pragma unroll
+            for (int rt = 0; rt < RT; rt++)
+                sc[rt][m][0] = sc[rt][m][1] = sc[rt][m][2] = sc[rt][m][3] = 0.f;
 #pragma unroll
             for (int u = 0; u < 4 * NC; u++) {
-                const uint32_t w = word(kr[n * NC + (u >> 2)], u & 3);
-                uint32_t af[4] = {qf[u][0], 0u, qf[u][RT], 0u};
-                if (RT == 2) {
-                    af[1] = qf[u][1];
-                    af[3] = qf[u][RT + 1];
-                }
-                mma_f16(sc[n], af, e4m3x2_to_f16x2(w), e4m3x2_to_f16x2(w >> 16));
+                const uint32_t wa = word(ka[u >> 2], u & 3), wb = word(kb[u >> 2], u & 3);
+                const uint32_t af[4] = {e4m3x2_to_f16x2(wa), e4m3x2_to_f16x2(wb), e4m3x2_to_f16x2(wa >> 16),
+                                        e4m3x2_to_f16x2(wb >> 16)};
+#pragma unroll
+                for (int rt = 0; rt < RT; rt++)
+                    mma_f16(sc[rt][m], af, qf[u][2 * rt], qf[u][2 * rt + 1]);
             }
         }
         if (next >= 0)
-            load_k(next);
-        // P of rows g (and g + 8), keys 16 t + 2 n, + 1
-        uint32_t pf[KN][RT];
-        float pinv[RT], wsum[2 * KN];
+            load(c.k_codes, kbuf, kbar, next);
+        // P^T: the B operand of word m is keys 16 t + 4 m .. + 3 of query g
+        uint32_t pf[RT][4][2];
+        float pinv[RT][2], wsum[8];
 #pragma unroll
-        for (int e = 0; e < 2 * KN; e++)
+        for (int e = 0; e < 8; e++)
             wsum[e] = 0.f;
 #pragma unroll
         for (int rt = 0; rt < RT; rt++) {
-            const bool live = g + 8 * rt < rows;
-            const float f = 0.5f * ks * qinv[rt];
-            const float *br = bias + (g + 8 * rt) * kBiasLd + 16 * t;
-            float pv[2 * KN], m = 0.f;
+            const bool live[2] = {8 * rt + 2 * t < rows, 8 * rt + 2 * t + 1 < rows};
+            const float f[2] = {0.5f * ks * qinv[rt][0], 0.5f * ks * qinv[rt][1]};
+            float m[2] = {0.f, 0.f};
 #pragma unroll
-            for (int e4 = 0; e4 < 2 * KN; e4 += 4) {
-                const float4 b4 = live ? *reinterpret_cast<const float4 *>(br + e4) : make_float4(0.f, 0.f, 0.f, 0.f);
-                const float bb[4] = {b4.x, b4.y, b4.z, b4.w};
+            for (int i = 0; i < 8; i++) {  // key key0 + 4 (i / 2) + 2 (i % 2)
+                const int key = key0 + 2 * i;
+                const float2 bb = *reinterpret_cast<const float2 *>(bias + key * kBiasLd + 8 * rt + 2 * t);
+                float *y = &sc[rt][i >> 1][2 * (i & 1)];
 #pragma unroll
-                for (int e = e4; e < e4 + 4; e++) {
-                    const float hh = fmaf(sc[e >> 1][2 * rt + (e & 1)], f, 0.5f * bb[e - e4]);
-                    float th;
-                    asm("tanh.approx.f32 %0, %1;" : "=f"(th) : "f"(hh));
-                    pv[e] = live && 16 * t + e < count ? fmaf(hh, th, hh) : 0.f;
-                    m = fmaxf(m, fabsf(pv[e]));
-                    wsum[e] += fabsf(pv[e]);
+                for (int e = 0; e < 2; e++) {
+                    const float hh = fmaf(y[e], f[e], 0.5f * (e ? bb.y : bb.x));
+                    y[e] = live[e] && key < count ? fmaf(hh, tanh_approx(hh), hh) : 0.f;
+                    m[e] = fmaxf(m[e], fabsf(y[e]));
+                    wsum[i] += fabsf(y[e]);
                 }
             }
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-            const float pr = to_range(m, &pinv[rt]);
+            float pr[2];
 #pragma unroll
-            for (int n = 0; n < KN; n++)
-                pf[n][rt] = pack_f16(pv[2 * n] * pr, pv[2 * n + 1] * pr);
-            pinv[rt] *= vs;
+            for (int e = 0; e < 2; e++) {
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1)
+                    m[e] = fmaxf(m[e], __shfl_xor_sync(0xffffffffu, m[e], x));
+                pr[e] = to_range(m[e], &pinv[rt][e]);
+                pinv[rt][e] *= vs;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                pf[rt][i >> 1][i & 1] = transpose8(pack_f16(sc[rt][i >> 1][2 * (i & 1)] * pr[0], sc[rt][i >> 1][2 * (i & 1) + 1] * pr[1]));
         }
         if (wplane) {
-            if (rows > 1) {
 #pragma unroll
-                for (int e = 0; e < 2 * KN; e++) {
-                    wsum[e] += __shfl_xor_sync(0xffffffffu, wsum[e], 4);
-                    wsum[e] += __shfl_xor_sync(0xffffffffu, wsum[e], 8);
-                    wsum[e] += __shfl_xor_sync(0xffffffffu, wsum[e], 16);
+            for (int i = 0; i < 8; i++) {
+                if (rows > 2) {
+                    wsum[i] += __shfl_xor_sync(0xffffffffu, wsum[i], 1);
+                    wsum[i] += __shfl_xor_sync(0xffffffffu, wsum[i], 2);
                 }
+                if (t == 0)  // behind the end: zeros, within the plane's whole pages
+                    wplane[p * kPage + key0 + 2 * i] = wsum[i];
             }
-            if (g == 0)
-#pragma unroll
-                for (int e = 0; e < 2 * KN; e += 4)  // behind the end: zeros, within the plane's whole pages
-                    *reinterpret_cast<float4 *>(wplane + p * kPage + 16 * t + e) =
-                        make_float4(wsum[e], wsum[e + 1], wsum[e + 2], wsum[e + 3]);
         }
-        if (count < kPage) {  // codes behind the last token may be anything
-            const int n = count - 16 * t;
-            uint32_t m[4];
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(vbar, loads & 1, &abort_flag, c.hdr))))
+            break;
+        uint32_t keep[4];  // codes behind the last token may be anything
 #pragma unroll
-            for (int e = 0; e < 4; e++)
-                m[e] = n >= 4 * e + 4 ? 0xffffffffu : n <= 4 * e ? 0u : (1u << (8 * (n - 4 * e))) - 1u;
-#pragma unroll
-            for (int i = 0; i < VN; i++)
-                vr[i] = make_uint4(vr[i].x & m[0], vr[i].y & m[1], vr[i].z & m[2], vr[i].w & m[3]);
+        for (int e = 0; e < 4; e++) {
+            const int n = count - 16 * t - 4 * e;
+            keep[e] = n >= 4 ? 0xffffffffu : n <= 0 ? 0u : (1u << (8 * n)) - 1u;
         }
+        const unsigned char *vrow = vbuf + g * kPage + 16 * t;
 #pragma unroll
         for (int n = 0; n < VN; n++) {
-            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+            const uint4 va = *reinterpret_cast<const uint4 *>(vrow + n * 16 * kPage);
+            const uint4 vb = *reinterpret_cast<const uint4 *>(vrow + (n * 16 + 8) * kPage);
+            float acc[RT][4];
+#pragma unroll
+            for (int rt = 0; rt < RT; rt++)
+                acc[rt][0] = acc[rt][1] = acc[rt][2] = acc[rt][3] = 0.f;
 #pragma unroll
             for (int st = 0; st < 4; st++) {
-                const uint32_t w = word(vr[n], st);
-                uint32_t af[4] = {pf[2 * st][0], 0u, pf[2 * st + 1][0], 0u};
-                if (RT == 2) {
-                    af[1] = pf[2 * st][RT - 1];
-                    af[3] = pf[2 * st + 1][RT - 1];
-                }
-                mma_f16(acc, af, e4m3x2_to_f16x2(w), e4m3x2_to_f16x2(w >> 16));
+                const uint32_t wa = word(va, st) & keep[st], wb = word(vb, st) & keep[st];
+                const uint32_t af[4] = {e4m3x2_to_f16x2(wa), e4m3x2_to_f16x2(wb), e4m3x2_to_f16x2(wa >> 16),
+                                        e4m3x2_to_f16x2(wb >> 16)};
+#pragma unroll
+                for (int rt = 0; rt < RT; rt++)
+                    mma_f16(acc[rt], af, pf[rt][st][0], pf[rt][st][1]);
             }
 #pragma unroll
-            for (int e = 0; e < 2 * RT; e++)
-                o[n][e] = fmaf(acc[e], pinv[e >> 1], o[n][e]);
+            for (int rt = 0; rt < RT; rt++)
+#pragma unroll
+                for (int e = 0; e < 4; e++)
+                    o[rt][n][e] = fmaf(acc[rt][e], pinv[rt][e & 1], o[rt][n][e]);
         }
         if (next >= 0)
-            load_v(next);
+            load(c.v_codes, vbuf, vbar, next);
         page = next;
+        loads++;
     }
     // the warps' sums, in order
     __syncthreads();
+    if (abort_flag)
+        return;  // a copy never came: flagged, the output is incomplete
+    float *sums = reinterpret_cast<float *>(smem);
 #pragma unroll
     for (int rt = 0; rt < RT; rt++)
-        if (g + 8 * rt < rows)
 #pragma unroll
-            for (int n = 0; n < VN; n++)
-                *reinterpret_cast<float2 *>(smem + (warp * R + g + 8 * rt) * D + 8 * n + 2 * t) =
-                    make_float2(o[n][2 * rt], o[n][2 * rt + 1]);
+        for (int e = 0; e < 2; e++)
+            if (8 * rt + 2 * t + e < rows)
+#pragma unroll
+                for (int n = 0; n < VN; n++) {
+                    float *dst = sums + (warp * R + 8 * rt + 2 * t + e) * D + 16 * n + g;
+                    dst[0] = o[rt][n][e];
+                    dst[8] = o[rt][n][2 + e];
+                }
     __syncthreads();
     for (int i = threadIdx.x; i < rows * D; i += kWarps * 32) {
         float sum = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; w++)
-            sum += smem[w * R * D + i];
+            sum += sums[w * R * D + i];
         a.part_o[(((int64_t)part * c.T + s.s0 + r0 + i / D) * c.H + h) * D + i % D] = sum;
     }
 }
@@ -302,8 +349,11 @@ cache_attn_rows_kernel(const CacheAttnArgs a)
 template <int D, int RT>
 cudaError_t rows_launch(const CacheAttnArgs &a, cudaStream_t stream)
 {
-    constexpr int bytes = kWarps * 8 * RT * std::max(D, kBiasLd) * 4;
-    static_assert(bytes <= 48 * 1024, "within the default dynamic shared memory");
+    constexpr int bytes = kWarps * (2 * kPage * D + kPage * (8 * RT + 2) * 4);
+    static_assert(8 * RT * D * 4 <= 2 * kPage * D, "the sums fit where the blocks were");
+    const cudaError_t e = cudaFuncSetAttribute(cache_attn_rows_kernel<D, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess)
+        return e;
     const int64_t grid = (int64_t)a.c.B * a.plan.nsplit * a.plan.qtiles * a.c.H;
     cache_attn_rows_kernel<D, RT><<<(unsigned)grid, kWarps * 32, bytes, stream>>>(a);
     return cudaGetLastError();
