@@ -61,8 +61,9 @@ __device__ __forceinline__ int table_page(const int32_t *table, const CacheCall 
     return page >= 0 && page < c.num_pages ? page : -1;
 }
 
-// weights_out of cached token j of sequence b: what it had plus its planes, in order.
-__device__ __forceinline__ void cache_join_weight(const CacheAttnArgs &a, int b, int j)
+// weights_out of cached tokens j .. j + 3 of sequence b (j a multiple of 4): what they
+// had plus their planes, in order.
+__device__ __forceinline__ void cache_join_weights(const CacheAttnArgs &a, int b, int j)
 {
     const CacheCall &c = a.c;
     const CacheSeq s = cache_seq(c, b);
@@ -72,11 +73,19 @@ __device__ __forceinline__ void cache_join_weight(const CacheAttnArgs &a, int b,
     if (page < 0)
         return;
     const int planes = (s.n + a.plan.plane_rows - 1) / a.plan.plane_rows * c.H;
-    float sum = 0.f;
-    for (int p = 0; p < planes; p++)
-        sum += a.part_w[((int64_t)p * c.B + b) * a.plan.lcap + j];
-    const int64_t at = (int64_t)page * kPage + j % kPage;
-    a.weights_out[at] = fmaf(fabsf(a.inv_n), sum, c.weights ? c.weights[at] : 0.f);
+    const int64_t at = (int64_t)page * kPage + j % kPage, step = (int64_t)c.B * a.plan.lcap;
+    const float *w = a.part_w + b * a.plan.lcap + j;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int p = 0; p < planes; p++) {
+        const float4 y = *reinterpret_cast<const float4 *>(w + p * step);
+        sum.x += y.x, sum.y += y.y, sum.z += y.z, sum.w += y.w;
+    }
+    const float add[4] = {sum.x, sum.y, sum.z, sum.w}, scale = fabsf(a.inv_n);
+#pragma unroll
+    for (int e = 0; e < 4; e++)
+        if (j + e < s.len)
+            a.weights_out[at + e] = fmaf(scale, add[e], c.weights ? c.weights[at + e] : 0.f);
 }
 
 // ---- E4M3 ---------------------------------------------------------------------

@@ -130,8 +130,15 @@ cache_attn_f32_kernel(const CacheAttnArgs a)
     }
 }
 
-__device__ __forceinline__ void put(float *p, float x) { *p = x; }
-__device__ __forceinline__ void put(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
+__device__ __forceinline__ void put4(float *p, const float *y)
+{
+    *reinterpret_cast<float4 *>(p) = make_float4(y[0], y[1], y[2], y[3]);
+}
+
+__device__ __forceinline__ void put4(__nv_bfloat16 *p, const float *y)
+{
+    *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
+}
 
 // Adds the parts: blocks [0, row_blocks * B) the output's rows, the others the weights.
 template <typename T>
@@ -146,23 +153,26 @@ cache_join_kernel(const CacheAttnArgs a, int row_blocks, int w_blocks)
         if (s.bits && chunk == 0 && threadIdx.x == 0)
             atomicOr(&c.hdr->flag, s.bits);
         const int nsp = ((s.len + kPage - 1) / kPage + a.plan.split_pages - 1) / a.plan.split_pages;
-        const int64_t at = (int64_t)chunk * 1024 + threadIdx.x, end = (int64_t)s.n * width;
-        T *out = static_cast<T *>(a.out);
-        const T *add = static_cast<const T *>(a.addend);
-        for (int64_t e = at; e < min(end, (int64_t)(chunk + 1) * 1024); e += 256) {
-            const int64_t i = s.s0 * width + e;
-            float sum = 0.f;
-            for (int p = 0; p < nsp; p++)
-                sum += a.part_o[p * c.T * width + i];
-            sum *= a.inv_n;
-            if (add)
-                sum += to_float(add[i]);
-            put(out + i, sum);
+        const int64_t e = ((int64_t)chunk * 256 + threadIdx.x) * 4;  // four elements of a row
+        if (e >= (int64_t)s.n * width)
+            return;
+        const int64_t i = s.s0 * width + e;
+        float y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+        for (int p = 0; p < nsp; p++) {
+            const float4 v = *reinterpret_cast<const float4 *>(a.part_o + p * c.T * width + i);
+            y[0] += v.x, y[1] += v.y, y[2] += v.z, y[3] += v.w;
         }
+        T *out = static_cast<T *>(a.out) + i;
+        const T *add = static_cast<const T *>(a.addend);
+#pragma unroll
+        for (int k = 0; k < 4; k++)
+            y[k] = y[k] * a.inv_n + (add ? to_float(add[i + k]) : 0.f);
+        put4(out, y);
         return;
     }
     const int x = blockIdx.x - row_blocks * c.B;
-    cache_join_weight(a, x / w_blocks, (x % w_blocks) * 256 + threadIdx.x);
+    cache_join_weights(a, x / w_blocks, ((x % w_blocks) * 256 + threadIdx.x) * 4);
 }
 
 int row_blocks(const CacheCall &c)  // one at least: it reports a sequence that was dropped
@@ -174,7 +184,7 @@ template <typename T>
 cudaError_t join(const CacheAttnArgs &a, cudaStream_t stream)
 {
     const CacheCall &c = a.c;
-    const int rows = row_blocks(c), w_blocks = a.weights_out ? (c.max_cache_len + 255) / 256 : 0;
+    const int rows = row_blocks(c), w_blocks = a.weights_out ? (c.max_cache_len + 1023) / 1024 : 0;
     cache_join_kernel<T><<<(unsigned)((rows + w_blocks) * c.B), 256, 0, stream>>>(a, rows, w_blocks);
     return cudaGetLastError();
 }

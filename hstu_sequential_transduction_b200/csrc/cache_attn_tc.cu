@@ -971,7 +971,7 @@ cache_tc_join_kernel(const CacheAttnArgs a, int ctas, int w_blocks)
         return;
     }
     x -= c.B;
-    cache_join_weight(a, x / w_blocks, (x % w_blocks) * 256 + threadIdx.x);
+    cache_join_weights(a, x / w_blocks, ((x % w_blocks) * 256 + threadIdx.x) * 4);
 }
 
 template <int D>
@@ -996,7 +996,7 @@ cudaError_t tc_launch(const CacheAttnArgs &a, cudaStream_t stream)
         if (e != cudaSuccess)
             return e;
     }
-    const int w_blocks = a.weights_out ? (c.max_cache_len + 255) / 256 : 0;
+    const int w_blocks = a.weights_out ? (c.max_cache_len + 1023) / 1024 : 0;
     const int64_t grid = 16LL * a.plan.ctas + c.B + (int64_t)w_blocks * c.B;
     cache_tc_join_kernel<D><<<(unsigned)grid, 256, 0, stream>>>(a, a.plan.ctas, w_blocks);
     return cudaGetLastError();

@@ -89,6 +89,13 @@ def load_library(allow_build: bool = True) -> ctypes.CDLL:
             lib.hstu_version.restype = ctypes.c_int
             for name in EXPORTED[2:]:
                 getattr(lib, name).restype = ctypes.c_int
+            # the cache's calls come once per token: with argument types they take plain integers
+            p, i, n, z = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+            lib.hstu_cache_append.argtypes = [p, i, i, i, n, p, n, p, n] + [p] * 9 + [z, p]
+            lib.hstu_cache_attn_workspace_size.argtypes = [p, p, i, i, p]
+            lib.hstu_cache_attn_fwd.argtypes = [p, p, i, p, n] + [p] * 12 + [z, p]
+            lib.hstu_cache_evict_workspace_size.argtypes = [p, i, i, i, p]
+            lib.hstu_cache_evict.argtypes = [p] + [i] * 5 + [p] * 7 + [z, p]
             lib.hstu_e4m3_weight_bytes.restype = ctypes.c_size_t
             lib.hstu_e4m3_weight_bytes.argtypes = [ctypes.c_int32, ctypes.c_int32]
             _lib = lib
@@ -450,6 +457,7 @@ class HstuCache:
         self.timestamps, self.positions, self.weights = timestamps, positions, weights
         self.num_pages, self.num_heads, self.head_dim = int(pages), int(heads), int(d)
         self.device = k_codes.device
+        self._structs = {}
 
     @classmethod
     def empty(cls, num_pages: int, num_heads: int, head_dim: int, device, weights: bool = True) -> "HstuCache":
@@ -462,12 +470,15 @@ class HstuCache:
                    z(pages, torch.float32), z(pages, torch.float32), z(tokens, torch.int64), z(tokens, torch.int32),
                    z(tokens, torch.float32) if weights else None)
 
-    def struct(self, max_pages: int) -> hstu_cache:
-        """The C struct of these tensors with block tables of max_pages columns."""
-        return hstu_cache(self.num_pages, self.num_heads, self.head_dim, int(max_pages), self.k_codes.data_ptr(),
-                          self.v_codes.data_ptr(), self.k_scale.data_ptr(), self.v_scale.data_ptr(),
-                          self.timestamps.data_ptr(), self.positions.data_ptr(),
-                          0 if self.weights is None else self.weights.data_ptr())
+    def struct(self, max_pages: int):
+        """The C struct of these tensors with block tables of max_pages columns, by reference."""
+        if max_pages not in self._structs:
+            self._structs[max_pages] = ctypes.byref(hstu_cache(
+                self.num_pages, self.num_heads, self.head_dim, int(max_pages), self.k_codes.data_ptr(),
+                self.v_codes.data_ptr(), self.k_scale.data_ptr(), self.v_scale.data_ptr(),
+                self.timestamps.data_ptr(), self.positions.data_ptr(),
+                0 if self.weights is None else self.weights.data_ptr()))
+        return self._structs[max_pages]
 
 
 def _same_device(t, name, device):
@@ -475,21 +486,28 @@ def _same_device(t, name, device):
         raise ValueError(f"{name} is on {t.device}, the cache on {device}")
 
 
-def _cache_ints(cache, block_table, **tensors):
-    """Checks the block table [B, max_pages] and the int32 tensors [B] beside it."""
-    _dev(block_table, "block_table", torch.int32)
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [num_seqs, max_pages]")
-    _same_device(block_table, "block_table", cache.device)
-    B = block_table.shape[0]
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        _dev(t, name, torch.int32)
-        if t.numel() != B:
-            raise ValueError(f"{name} has {t.numel()} entries for {B} sequences")
-        _same_device(t, name, cache.device)
-    return B
+def _on(device, t, name, dtype) -> int:
+    """The address of a dense tensor of this type on the cache's device; 0 for None."""
+    if t is None:
+        return 0
+    if t.dtype is not dtype or t.get_device() != device.index or not t.is_contiguous():
+        _dev(t, name, dtype)
+        _same_device(t, name, device)
+    return t.data_ptr()
+
+
+def _cache_table(cache, t, name, shape=None) -> int:
+    p = _on(cache.device, t, name, torch.int32)
+    if t is not None and (t.dim() != 2 if shape is None else t.shape != shape):
+        raise ValueError(f"{name} must be [num_seqs, max_pages]")
+    return p
+
+
+def _cache_ints(cache, B, t, name) -> int:
+    p = _on(cache.device, t, name, torch.int32)
+    if t is not None and t.numel() != B:
+        raise ValueError(f"{name} has {t.numel()} entries for {B} sequences")
+    return p
 
 
 def _cache_rows(cache, name, t):
@@ -502,21 +520,17 @@ def _cache_rows(cache, name, t):
     st = t.stride()
     if t.numel() and (st[2] != 1 or (H > 1 and st[1] != d)):
         raise ValueError(f"{name} must have dense rows")
-    _same_device(t, name, cache.device)
+    if t.get_device() != cache.device.index:
+        _same_device(t, name, cache.device)
     return st[0] if t.shape[0] > 1 else H * d
 
 
-def _cache_stream(cache, stream):
-    return _stream(torch.cuda.current_stream(cache.device) if stream is None else stream)
-
-
 def _cache_tokens(cache, B, T, seq_offsets, timestamps):
-    _dev(seq_offsets, "seq_offsets", torch.int64)
-    _dev(timestamps, "timestamps", torch.int64)
+    off = _on(cache.device, seq_offsets, "seq_offsets", torch.int64)
+    ts = _on(cache.device, timestamps, "timestamps", torch.int64)
     if seq_offsets.numel() != B + 1 or timestamps.numel() != T:
         raise ValueError(f"seq_offsets needs {B + 1} entries and timestamps {T}")
-    _same_device(seq_offsets, "seq_offsets", cache.device)
-    _same_device(timestamps, "timestamps", cache.device)
+    return off, ts
 
 
 def _cache_workspace(cache, workspace, need):
@@ -524,6 +538,23 @@ def _cache_workspace(cache, workspace, need):
         return alloc_workspace(need, cache.device)
     _same_device(workspace, "workspace", cache.device)
     return workspace
+
+
+def _cache_call(cache, name, stream, *args):
+    """Calls into the library on the cache's device and, by default, that device's current stream."""
+    fn = getattr(load_library(), name)
+    if torch.cuda.current_device() == cache.device.index:
+        status = fn(*args, _cache_stream(cache, stream))
+    else:
+        with torch.cuda.device(cache.device):
+            status = fn(*args, _cache_stream(cache, stream))
+    _check(name, status)
+
+
+def _cache_stream(cache, stream):
+    if stream is None:
+        stream = torch.cuda.current_stream(cache.device)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def hstu_cache_append_workspace_size() -> int:
@@ -537,23 +568,23 @@ def hstu_cache_append(k, v, cache: HstuCache, block_table, cache_lens, seq_pos, 
     """Append each sequence's history tokens to the cache: k, v [T, H, d] (rows may lie
     further apart, as in a projection's output).  Returns (new_lens, new_pos) [B] int32;
     seq_pos None means cache_lens (nothing was evicted before)."""
-    B = _cache_ints(cache, block_table, cache_lens=cache_lens, seq_pos=seq_pos, num_targets=num_targets,
-                    new_lens=new_lens, new_pos=new_pos)
+    table = _cache_table(cache, block_table, "block_table")
+    B, cols = block_table.shape
+    lens, pos, nt = (_cache_ints(cache, B, t, n) for t, n in ((cache_lens, "cache_lens"), (seq_pos, "seq_pos"),
+                                                              (num_targets, "num_targets")))
     sk, sv = _cache_rows(cache, "k", k), _cache_rows(cache, "v", v)
     if v.dtype != k.dtype or v.shape != k.shape:
         raise ValueError("k and v must have one type and shape")
-    _cache_tokens(cache, B, k.shape[0], seq_offsets, timestamps)
+    T = k.shape[0]
+    off, ts = _cache_tokens(cache, B, T, seq_offsets, timestamps)
     if new_lens is None:
         new_lens = torch.empty_like(cache_lens)
     if new_pos is None:
         new_pos = torch.empty_like(cache_lens)
     workspace = _cache_workspace(cache, workspace, 256)
-    with torch.cuda.device(cache.device):
-        _check("hstu_cache_append", load_library().hstu_cache_append(
-            ctypes.byref(cache.struct(block_table.shape[1])), _dtype_code(k), B, int(max_seq_len),
-            ctypes.c_int64(k.shape[0]), _ptr(k), ctypes.c_int64(sk), _ptr(v), ctypes.c_int64(sv), _ptr(seq_offsets),
-            _ptr(timestamps), _ptr(num_targets), _ptr(block_table), _ptr(cache_lens), _ptr(seq_pos), _ptr(new_lens),
-            _ptr(new_pos), _ptr(workspace), ctypes.c_size_t(workspace.numel()), _cache_stream(cache, stream)))
+    _cache_call(cache, "hstu_cache_append", stream, cache.struct(cols), _dtype_code(k), B, max_seq_len, T, k.data_ptr(), sk,
+                v.data_ptr(), sv, off, ts, nt, table, lens, pos, _cache_ints(cache, B, new_lens, "new_lens"),
+                _cache_ints(cache, B, new_pos, "new_pos"), workspace.data_ptr(), workspace.numel())
     return new_lens, new_pos
 
 
@@ -570,8 +601,7 @@ def hstu_cache_attn_workspace_size(q, cache: HstuCache, block_table, rab_pos, ra
     desc = _cache_attn_desc(q, block_table, rab_pos, rab_time, max_seq_len, inv_n, pos_lo, pos_hi, cand_own_index)
     n = ctypes.c_size_t(0)
     _check("hstu_cache_attn_workspace_size", load_library().hstu_cache_attn_workspace_size(
-        ctypes.byref(desc), ctypes.byref(cache.struct(block_table.shape[1])), int(max_cache_len), int(weights),
-        ctypes.byref(n)))
+        ctypes.byref(desc), cache.struct(block_table.shape[1]), max_cache_len, int(weights), ctypes.byref(n)))
     return n.value
 
 
@@ -583,42 +613,35 @@ def hstu_cache_attn_fwd(q, cache: HstuCache, block_table, cache_lens, seq_pos, s
     (hstu_attn_fwd over the new tokens themselves; may be `out`).  weights_out
     [pages, 64] float32 receives the cached tokens' accumulated attention weight; it
     may be cache.weights."""
-    B = _cache_ints(cache, block_table, cache_lens=cache_lens, seq_pos=seq_pos, num_targets=num_targets)
+    table = _cache_table(cache, block_table, "block_table")
+    B, cols = block_table.shape
+    lens, pos, nt = (_cache_ints(cache, B, t, n) for t, n in ((cache_lens, "cache_lens"), (seq_pos, "seq_pos"),
+                                                              (num_targets, "num_targets")))
     sq = _cache_rows(cache, "q", q)
-    _cache_tokens(cache, B, q.shape[0], seq_offsets, timestamps)
-    for name, t in (("rab_pos", rab_pos), ("rab_time", rab_time)):
-        _dev(t, name, torch.float32)
-        _same_device(t, name, cache.device)
+    off, ts = _cache_tokens(cache, B, q.shape[0], seq_offsets, timestamps)
+    rp = _on(cache.device, rab_pos, "rab_pos", torch.float32)
+    rt = _on(cache.device, rab_time, "rab_time", torch.float32)
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = torch.empty(q.shape, dtype=q.dtype, device=cache.device)
     for name, t in (("addend", addend), ("out", out)):
-        if t is None:
-            continue
-        _dev(t, name, q.dtype)
-        if t.shape != q.shape:
+        if t is not None and t.shape != q.shape:
             raise ValueError(f"{name} must have q's shape")
-        _same_device(t, name, cache.device)
-    if weights_out is not None:
-        _dev(weights_out, "weights_out", torch.float32)
-        if tuple(weights_out.shape) != (cache.num_pages, HSTU_CACHE_PAGE):
-            raise ValueError("weights_out must be [pages, 64]")
-        _same_device(weights_out, "weights_out", cache.device)
-    desc = _cache_attn_desc(q, block_table, rab_pos, rab_time, max_seq_len, inv_n, pos_lo, pos_hi, cand_own_index)
-    pool = cache.struct(block_table.shape[1])
-    lib = load_library()
-    with torch.cuda.device(cache.device):
-        if workspace is None:
-            n = ctypes.c_size_t(0)
-            _check("hstu_cache_attn_workspace_size", lib.hstu_cache_attn_workspace_size(
-                ctypes.byref(desc), ctypes.byref(pool), int(max_cache_len), int(weights_out is not None),
-                ctypes.byref(n)))
-            workspace = alloc_workspace(n.value, q.device)
-        _same_device(workspace, "workspace", cache.device)
-        _check("hstu_cache_attn_fwd", lib.hstu_cache_attn_fwd(
-            ctypes.byref(desc), ctypes.byref(pool), int(max_cache_len), _ptr(q), ctypes.c_int64(sq),
-            _ptr(seq_offsets), _ptr(timestamps), _ptr(num_targets), _ptr(rab_pos), _ptr(rab_time), _ptr(block_table),
-            _ptr(cache_lens), _ptr(seq_pos), _ptr(addend), _ptr(weights_out), _ptr(out), _ptr(workspace),
-            ctypes.c_size_t(workspace.numel()), _cache_stream(cache, stream)))
+    if weights_out is not None and tuple(weights_out.shape) != (cache.num_pages, HSTU_CACHE_PAGE):
+        raise ValueError("weights_out must be [pages, 64]")
+    desc = ctypes.byref(_cache_attn_desc(q, block_table, rab_pos, rab_time, max_seq_len, inv_n, pos_lo, pos_hi,
+                                         cand_own_index))
+    pool = cache.struct(cols)
+    if workspace is None:
+        n = ctypes.c_size_t(0)
+        with torch.cuda.device(cache.device):
+            _check("hstu_cache_attn_workspace_size", load_library().hstu_cache_attn_workspace_size(
+                desc, pool, max_cache_len, int(weights_out is not None), ctypes.byref(n)))
+        workspace = alloc_workspace(n.value, cache.device)
+    _same_device(workspace, "workspace", cache.device)
+    _cache_call(cache, "hstu_cache_attn_fwd", stream, desc, pool, max_cache_len, q.data_ptr(), sq, off, ts, nt, rp, rt,
+                table, lens, pos, _on(cache.device, addend, "addend", q.dtype),
+                _on(cache.device, weights_out, "weights_out", torch.float32), _on(cache.device, out, "out", q.dtype),
+                workspace.data_ptr(), workspace.numel())
     return out
 
 
@@ -626,8 +649,7 @@ def hstu_cache_evict_workspace_size(cache: HstuCache, block_table, *, keep: int,
                                     recent: int = 0) -> int:
     n = ctypes.c_size_t(0)
     _check("hstu_cache_evict_workspace_size", load_library().hstu_cache_evict_workspace_size(
-        ctypes.byref(cache.struct(block_table.shape[1])), block_table.shape[0], int(max_cache_len), int(keep),
-        ctypes.byref(n)))
+        cache.struct(block_table.shape[1]), block_table.shape[0], max_cache_len, keep, ctypes.byref(n)))
     return n.value
 
 
@@ -637,33 +659,28 @@ def hstu_cache_evict(cache: HstuCache, block_table, cache_lens, new_pages, *, ke
     """Cut every sequence of more than `keep` tokens to its first `first`, its last
     `recent` and, of the rest, the tokens of largest weight; they move into the pages
     of new_pages [B, max_pages].  Returns (new_table, new_lens, kept [B, keep])."""
-    B = _cache_ints(cache, block_table, cache_lens=cache_lens, new_lens=new_lens)
+    table = _cache_table(cache, block_table, "block_table")
+    B, cols = block_table.shape
     if cache.weights is None:
         raise ValueError("eviction needs the cache's weights")
-    for name, t in (("new_pages", new_pages), ("new_table", new_table)):
-        if t is None:
-            continue
-        _dev(t, name, torch.int32)
-        if t.shape != block_table.shape:
-            raise ValueError(f"{name} must have block_table's shape")
-        _same_device(t, name, cache.device)
-    need = hstu_cache_evict_workspace_size(cache, block_table, keep=keep, max_cache_len=max_cache_len)
     if new_table is None:
         new_table = torch.empty_like(block_table)
     if new_lens is None:
         new_lens = torch.empty_like(cache_lens)
     if kept is None:
-        kept = torch.empty((B, int(keep)), dtype=torch.int32, device=cache.device)
-    _dev(kept, "kept", torch.int32)
-    if tuple(kept.shape) != (B, int(keep)):
+        kept = torch.empty((B, keep), dtype=torch.int32, device=cache.device)
+    if tuple(kept.shape) != (B, keep):
         raise ValueError(f"kept must be [{B}, {keep}]")
-    _same_device(kept, "kept", cache.device)
-    workspace = _cache_workspace(cache, workspace, need)
-    with torch.cuda.device(cache.device):
-        _check("hstu_cache_evict", load_library().hstu_cache_evict(
-            ctypes.byref(cache.struct(block_table.shape[1])), B, int(max_cache_len), int(keep), int(first),
-            int(recent), _ptr(block_table), _ptr(cache_lens), _ptr(new_pages), _ptr(new_table), _ptr(new_lens),
-            _ptr(kept), _ptr(workspace), ctypes.c_size_t(workspace.numel()), _cache_stream(cache, stream)))
+    if workspace is None:
+        workspace = alloc_workspace(hstu_cache_evict_workspace_size(cache, block_table, keep=keep,
+                                                                    max_cache_len=max_cache_len), cache.device)
+    _same_device(workspace, "workspace", cache.device)
+    _cache_call(cache, "hstu_cache_evict", stream, cache.struct(cols), B, max_cache_len, keep, first, recent, table,
+                _cache_ints(cache, B, cache_lens, "cache_lens"),
+                _cache_table(cache, new_pages, "new_pages", block_table.shape),
+                _cache_table(cache, new_table, "new_table", block_table.shape),
+                _cache_ints(cache, B, new_lens, "new_lens"), _on(cache.device, kept, "kept", torch.int32),
+                workspace.data_ptr(), workspace.numel())
     return new_table, new_lens, kept
 
 
