@@ -21,24 +21,35 @@ namespace hstu {
 
 namespace {
 
-// eight elements to floats
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float *v)
-{
-    const uint4 w = *reinterpret_cast<const uint4 *>(p);
-    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int e = 0; e < 4; e++) {
-        v[2 * e] = __uint_as_float(ww[e] << 16);
-        v[2 * e + 1] = __uint_as_float(ww[e] & 0xffff0000u);
+// eight elements as they lie in memory
+struct Eight16 {
+    uint4 w;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { w = *reinterpret_cast<const uint4 *>(p); }
+    __device__ __forceinline__ void zero() { w = make_uint4(0u, 0u, 0u, 0u); }
+    __device__ __forceinline__ float get(int e) const
+    {
+        const uint32_t x = e < 2 ? w.x : e < 4 ? w.y : e < 6 ? w.z : w.w;
+        return __uint_as_float(e & 1 ? x & 0xffff0000u : x << 16);
     }
-}
+};
 
-__device__ __forceinline__ void load8(const float *p, float *v)
-{
-    const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-}
+struct Eight32 {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float *p)
+    {
+        a = reinterpret_cast<const float4 *>(p)[0];
+        b = reinterpret_cast<const float4 *>(p)[1];
+    }
+    __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ float get(int e) const
+    {
+        const float4 &f = e < 4 ? a : b;
+        return (e & 3) == 0 ? f.x : (e & 3) == 1 ? f.y : (e & 3) == 2 ? f.z : f.w;
+    }
+};
+
+template <typename T> struct EightOf { using type = Eight32; };
+template <> struct EightOf<__nv_bfloat16> { using type = Eight16; };
 
 // four codes re-rounded after a change of scale (ratio = old scale / new scale)
 __device__ __forceinline__ uint32_t rescale4(uint32_t codes, float ratio)
@@ -78,37 +89,37 @@ cache_append_kernel(const CacheCall c, const T *__restrict__ k, int64_t ldk, con
     const int end = min(s.len + count - blk * kPage, kPage);
     if (a >= end)
         return;
-    const int page = table_page(c.table, c, b, blk);
-    if (page < 0) {
-        if (h == 0 && threadIdx.x == 0)
-            atomicOr(&c.hdr->flag, FLAG_CACHE_PAGE);
-        return;
-    }
     const int part = threadIdx.x % (D / 8), quad = threadIdx.x / (D / 8);
     const int t0 = 4 * quad;
     // row of slot t: the sequence's token blk * 64 + t - len
     const int64_t row0 = s.s0 + (int64_t)blk * kPage - s.len;
 
-    float x[4][8], y[4][8];
+    typename EightOf<T>::type x[4], y[4];
     uint32_t mk = 0, mv = 0;
 #pragma unroll
     for (int t = 0; t < 4; t++) {
-        const bool fresh = t0 + t >= a && t0 + t < end;
-        if (fresh) {
-            load8(k + (row0 + t0 + t) * ldk + (int64_t)h * D + 8 * part, x[t]);
-            load8(v + (row0 + t0 + t) * ldv + (int64_t)h * D + 8 * part, y[t]);
+        if (t0 + t >= a && t0 + t < end) {
+            x[t].load(k + (row0 + t0 + t) * ldk + (int64_t)h * D + 8 * part);
+            y[t].load(v + (row0 + t0 + t) * ldv + (int64_t)h * D + 8 * part);
         } else {
-#pragma unroll
-            for (int e = 0; e < 8; e++)
-                x[t][e] = y[t][e] = 0.f;
+            x[t].zero();
+            y[t].zero();
         }
     }
+    const int page = table_page(c.table, c, b, blk);  // while the rows are on their way
+    if (page < 0) {
+        if (h == 0 && threadIdx.x == 0)
+            atomicOr(&c.hdr->flag, FLAG_CACHE_PAGE);
+        return;
+    }
+    const int64_t si = (int64_t)page * c.H + h;
+    const float kold = a > 0 ? c.k_scale[si] : 0.f, vold = a > 0 ? c.v_scale[si] : 0.f;
 #pragma unroll
     for (int t = 0; t < 4; t++)
 #pragma unroll
         for (int e = 0; e < 8; e++) {
-            mk = max(mk, __float_as_uint(x[t][e]) & 0x7fffffffu);
-            mv = max(mv, __float_as_uint(y[t][e]) & 0x7fffffffu);
+            mk = max(mk, __float_as_uint(x[t].get(e)) & 0x7fffffffu);
+            mv = max(mv, __float_as_uint(y[t].get(e)) & 0x7fffffffu);
         }
     mk = __reduce_max_sync(0xffffffffu, mk);
     mv = __reduce_max_sync(0xffffffffu, mv);
@@ -116,8 +127,6 @@ cache_append_kernel(const CacheCall c, const T *__restrict__ k, int64_t ldk, con
         smax[0][threadIdx.x >> 5] = mk;
         smax[1][threadIdx.x >> 5] = mv;
     }
-    const int64_t si = (int64_t)page * c.H + h;
-    const float kold = a > 0 ? c.k_scale[si] : 0.f, vold = a > 0 ? c.v_scale[si] : 0.f;
     __syncthreads();
     mk = mv = 0;
 #pragma unroll
@@ -139,8 +148,8 @@ cache_append_kernel(const CacheCall c, const T *__restrict__ k, int64_t ldk, con
         uint2 *dst = reinterpret_cast<uint2 *>(kc + (t0 + t) * D + 8 * part);
         if (t0 + t >= a && t0 + t < end) {
             uint2 w;
-            w.x = f32x2_to_e4m3x2(x[t][0] * ki, x[t][1] * ki) | (f32x2_to_e4m3x2(x[t][2] * ki, x[t][3] * ki) << 16);
-            w.y = f32x2_to_e4m3x2(x[t][4] * ki, x[t][5] * ki) | (f32x2_to_e4m3x2(x[t][6] * ki, x[t][7] * ki) << 16);
+            w.x = f32x2_to_e4m3x2(x[t].get(0) * ki, x[t].get(1) * ki) | (f32x2_to_e4m3x2(x[t].get(2) * ki, x[t].get(3) * ki) << 16);
+            w.y = f32x2_to_e4m3x2(x[t].get(4) * ki, x[t].get(5) * ki) | (f32x2_to_e4m3x2(x[t].get(6) * ki, x[t].get(7) * ki) << 16);
             *dst = w;
         } else if (t0 + t < a && kratio != 1.f) {
             const uint2 w = *dst;
@@ -154,7 +163,7 @@ cache_append_kernel(const CacheCall c, const T *__restrict__ k, int64_t ldk, con
         float y4[4];
 #pragma unroll
         for (int t = 0; t < 4; t++)
-            y4[t] = (part & 1) ? y[t][ee ^ 1] : y[t][ee];
+            y4[t] = (part & 1) ? y[t].get(ee ^ 1) : y[t].get(ee);
         uint32_t w = f32x2_to_e4m3x2(y4[0] * vi, y4[1] * vi) | (f32x2_to_e4m3x2(y4[2] * vi, y4[3] * vi) << 16);
         if (t0 < a || t0 + 4 > end) {  // some of these slots are not new: shifted if older, kept if behind the end
             const uint32_t was = *reinterpret_cast<const uint32_t *>(vc + d * kPage + t0);

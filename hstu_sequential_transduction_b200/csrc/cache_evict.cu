@@ -1,17 +1,18 @@
 // Eviction from the 8-bit key/value cache by accumulated attention weight.
 //
-// Select (one CTA per sequence): weights become integers that compare as the
-// weights do (NaN 0); four 8-bit histogram passes find the m-th largest of the
-// unprotected tokens; two ordered passes, in which a thread owns a run of
-// consecutive tokens, count and write the kept indices, ties at the threshold to
-// the lowest index.  Bound by latency: a few passes over 4 L bytes that stay in L2.
+// Select (one CTA per sequence): weights become integers that compare as the weights
+// do (NaN 0).  The m-th largest of the unprotected tokens is found bit by bit, each bit
+// one count of the keys at or above a candidate; the first 16,384 keys stay in
+// registers, sixteen a thread, so that a bit costs one barrier.  (Histograms of 8 bits
+// in shared memory took 30 us for 12,288 tokens: equal exponents crowd into few bins.)
+// Ballots and two scans then place the kept indices, ties to the lowest.
 //
-// Move (one CTA per new block and head): keys are gathered as rows; values are
-// stored transposed, so the source pages the block draws on are staged in shared
-// memory whole (rows padded to 17 words: the threads of a warp read one byte each
-// of 32 rows without a bank conflict) and the kept columns picked out.  The block
-// gets its own scale from the largest decoded magnitude.  Bound by HBM: the kept
-// keys and the source pages of the values are read once, the new block written.
+// Move (one CTA per new block and head, a thread per dim): keys are gathered as rows of
+// 16-byte pieces.  Values are stored transposed: a thread takes its dim's row of every
+// source page the block draws on, the next page's on its way meanwhile, through a
+// shared-memory row of its own (no barriers), and picks the kept bytes.  The block gets
+// its own scale from the largest decoded magnitude.  Bound by HBM: the kept keys and the
+// source pages of the values are read once, the new block written.
 #include <algorithm>
 
 #include "cache.cuh"
@@ -20,7 +21,6 @@ namespace hstu {
 
 namespace {
 
-constexpr int kSelThreads = 1024;
 
 __device__ __forceinline__ uint32_t weight_key(float w)
 {
@@ -30,45 +30,53 @@ __device__ __forceinline__ uint32_t weight_key(float w)
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// exclusive sum over the block's threads; *total the sum
-__device__ __forceinline__ int block_scan(int x, int *warp_sums, int *total)
+constexpr int kSelKeys = 16;  // keys a thread keeps in registers
+
+// sum over the block's threads; `slots`: 32 ints that no earlier call still reads
+template <int kWarps>
+__device__ __forceinline__ int block_sum(int x, int *slots)
 {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int inc = x;
+    x = __reduce_add_sync(0xffffffffu, x);
+    if ((threadIdx.x & 31) == 0)
+        slots[threadIdx.x >> 5] = x;
+    __syncthreads();
+    return __reduce_add_sync(0xffffffffu, (threadIdx.x & 31) < kWarps ? slots[threadIdx.x & 31] : 0);
+}
+
+// In place, exclusive prefix sums of counts[0, 16 kWarps); returns the total.
+template <int kWarps>
+__device__ __forceinline__ int scan_counts(int *counts, int *slots)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    __syncthreads();
+    int x = tid < kSelKeys * kWarps ? counts[tid] : 0, inc = x;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o)
             inc += y;
     }
-    __syncthreads();
     if (lane == 31)
-        warp_sums[warp] = inc;
+        slots[warp] = inc;
     __syncthreads();
-    if (warp == 0) {
-        int w = warp_sums[lane];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, w, o);
-            if (lane >= o)
-                w += y;
-        }
-        warp_sums[lane] = w;
-    }
+    const int mine = lane < kWarps ? slots[lane] : 0;
+    const int before = __reduce_add_sync(0xffffffffu, lane < warp ? mine : 0);
+    const int total = __reduce_add_sync(0xffffffffu, mine);
+    if (tid < kSelKeys * kWarps)
+        counts[tid] = before + inc - x;
     __syncthreads();
-    *total = warp_sums[31];
-    return inc - x + (warp ? warp_sums[warp - 1] : 0);
+    return total;
 }
 
+template <int kSelThreads>
 __global__ void __launch_bounds__(kSelThreads)
 cache_select_kernel(const CacheCall c, int keep, int first, int recent, const int32_t *__restrict__ new_pages,
                     int32_t *__restrict__ new_table, int32_t *__restrict__ new_lens, int32_t *__restrict__ kept,
                     uint32_t *__restrict__ keys, int64_t cap)
 {
-    __shared__ int hist[256];
-    __shared__ int warp_sums[32];
-    __shared__ int found[2];
-    const int b = blockIdx.x, tid = threadIdx.x;
+    constexpr int kSelWarps = kSelThreads / 32;
+    __shared__ int slots[2][32], counts[kSelKeys * kSelWarps];
+    const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const CacheSeq s = cache_seq(c, b);
     const int L = s.len;
     const bool moves = L > keep;
@@ -88,106 +96,128 @@ cache_select_kernel(const CacheCall c, int keep, int first, int recent, const in
     }
     const int late = min(keep, recent), early = min(min(keep - late, first), L - late);
     const int m = keep - late - early;  // of the tokens [early, L - late)
-    uint32_t *key = keys + (int64_t)b * cap;
+    constexpr int kRound = kSelKeys * kSelThreads;
+    uint32_t *rest = keys + (int64_t)b * cap;  // the keys from kRound on
     bool bad = false;
-    for (int j = tid; j < L; j += kSelThreads) {
+    auto open = [&](int j) { return j >= early && j < L - late; };
+    auto key_of = [&](int j) {  // 0 for a protected token too
         const int page = table_page(c.table, c, b, j / kPage);
         bad |= page < 0;
-        key[j] = page < 0 ? 0u : weight_key(c.weights[(int64_t)page * kPage + j % kPage]);
-    }
+        return page < 0 || !open(j) ? 0u : weight_key(c.weights[(int64_t)page * kPage + j % kPage]);
+    };
+    uint32_t key[kSelKeys];  // of tokens tid + 1024 i
+#pragma unroll
+    for (int i = 0; i < kSelKeys; i++)
+        key[i] = i * kSelThreads + tid < L ? key_of(i * kSelThreads + tid) : 0u;
+    for (int j = kRound + tid; j < L; j += kSelThreads)  // read again by this thread only
+        rest[j] = key_of(j);
     if (bad)
         atomicOr(&c.hdr->flag, FLAG_CACHE_PAGE);
-    __syncthreads();
-    // the m-th largest key: `prefix` after four passes; `left` of the tokens equal to it are kept
-    uint32_t prefix = 0, mask = 0;
-    int left = m;
-    for (int shift = 24; shift >= 0 && m > 0; shift -= 8) {
-        for (int i = tid; i < 256; i += kSelThreads)
-            hist[i] = 0;
-        __syncthreads();
-        for (int j = early + tid; j < L - late; j += kSelThreads) {
-            const uint32_t u = key[j];
-            if ((u & mask) == prefix)
-                atomicAdd(&hist[(u >> shift) & 255], 1);
-        }
-        __syncthreads();
-        if (tid < 32) {
-            // lane: bins 255 - 8 lane downwards; the bin in which the running count reaches `left`
-            int n[8], sum = 0;
+    // the largest value that at least m open keys reach (0 if m is 0: then nothing is taken)
+    uint32_t at = 0;
+    int turn = 0;
+    auto count_from = [&](uint32_t want) {  // open keys at or above it (want > 0: the closed ones are 0)
+        int n = 0;
 #pragma unroll
-            for (int e = 0; e < 8; e++) {
-                n[e] = hist[255 - 8 * tid - e];
-                sum += n[e];
-            }
-            int inc = sum;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, inc, o);
-                if (tid >= o)
-                    inc += y;
-            }
-            int run = inc - sum;
-#pragma unroll
-            for (int e = 0; e < 8; e++) {
-                if (run < left && run + n[e] >= left) {
-                    found[0] = 255 - 8 * tid - e;
-                    found[1] = left - run;
-                }
-                run += n[e];
-            }
-        }
-        __syncthreads();
-        prefix |= (uint32_t)found[0] << shift;
-        mask |= 255u << shift;
-        left = found[1];
-        __syncthreads();
+        for (int i = 0; i < kSelKeys; i++)
+            if (i * kSelThreads < L)
+                n += key[i] >= want;
+        for (int j = kRound + tid; j < L; j += kSelThreads)
+            n += rest[j] >= want;
+        return block_sum<kSelWarps>(n, slots[turn ^= 1]);
+    };
+    for (uint32_t bit = 0x80000000u; bit != 0 && m > 0; bit >>= 1) {
+        const int n = count_from(at | bit);
+        if (n >= m)
+            at |= bit;
+        if (n == m)  // exactly these
+            break;
     }
-    // ordered: thread t owns [t * run, (t + 1) * run)
-    const int run = (L + kSelThreads - 1) / kSelThreads;
-    const int j0 = min(tid * run, L), j1 = min(j0 + run, L);
-    int eq = 0, gt = 0;
-    for (int j = j0; j < j1; j++) {
-        const bool safe = j < early || j >= L - late;
-        const uint32_t u = key[j];
-        gt += safe || (m > 0 && u > prefix);
-        eq += !safe && m > 0 && u == prefix;
-    }
-    int total;
-    const int eq0 = block_scan(eq, warp_sums, &total);
-    // of this thread's ties, those among the first `left` of all
-    const int mine = max(0, min(eq, left - eq0));
-    int at = block_scan(gt + mine, warp_sums, &total);
-    int ties = mine;
-    for (int j = j0; j < j1; j++) {
-        const bool safe = j < early || j >= L - late;
-        const uint32_t u = key[j];
-        bool take = safe || (m > 0 && u > prefix);
-        if (!take && m > 0 && u == prefix && ties > 0) {
-            take = true;
-            ties--;
+    const int above = at == 0xffffffffu ? 0 : count_from(at + 1);
+    const int ties = m > 0 ? m - above : 0;  // of the keys equal to `at`, the first ones
+    // in rounds of 16 x 1024 tokens: what each warp's 32 tokens hold, scanned
+    const uint32_t below = (1u << lane) - 1u;
+    int ties_before = 0, out_before = 0;
+    for (int j0 = 0; j0 < L; j0 += kRound) {
+        if (j0 > 0)
+#pragma unroll
+            for (int i = 0; i < kSelKeys; i++)
+                key[i] = j0 + i * kSelThreads + tid < L ? rest[j0 + i * kSelThreads + tid] : 0u;
+        uint32_t safe = 0, tie = 0;  // bit i: token i of this thread
+#pragma unroll
+        for (int i = 0; i < kSelKeys; i++) {
+            const int j = j0 + i * kSelThreads + tid;
+            const bool is_tie = m > 0 && open(j) && key[i] == at;
+            const bool is_safe = j < L && (!open(j) || (m > 0 && key[i] > at));
+            safe |= (uint32_t)is_safe << i;
+            tie |= (uint32_t)is_tie << i;
+            const uint32_t votes = __ballot_sync(0xffffffffu, is_tie);
+            if (lane == 0)
+                counts[i * kSelWarps + warp] = __popc(votes);
         }
-        if (take)
-            out[at++] = j;
+        const int n_ties = scan_counts<kSelWarps>(counts, slots[turn ^= 1]);
+        uint32_t take = safe;
+#pragma unroll
+        for (int i = 0; i < kSelKeys; i++) {
+            const uint32_t votes = __ballot_sync(0xffffffffu, tie >> i & 1);
+            const int rank = ties_before + counts[i * kSelWarps + warp] + __popc(votes & below);
+            take |= (uint32_t)((tie >> i & 1) && rank < ties) << i;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kSelKeys; i++) {
+            const uint32_t votes = __ballot_sync(0xffffffffu, take >> i & 1);
+            if (lane == 0)
+                counts[i * kSelWarps + warp] = __popc(votes);
+        }
+        const int n_out = scan_counts<kSelWarps>(counts, slots[turn ^= 1]);
+#pragma unroll
+        for (int i = 0; i < kSelKeys; i++) {
+            const uint32_t votes = __ballot_sync(0xffffffffu, take >> i & 1);
+            if (take >> i & 1)
+                out[out_before + counts[i * kSelWarps + warp] + __popc(votes & below)] = j0 + i * kSelThreads + tid;
+        }
+        __syncthreads();
+        ties_before += n_ties;
+        out_before += n_out;
     }
 }
 
+// largest magnitude of four codes, as a code
+__device__ __forceinline__ uint32_t max_code(uint32_t w)
+{
+    const uint32_t m = w & 0x7f7f7f7fu, n = __vmaxu4(m, m >> 16);
+    return max(n & 255u, n >> 8 & 255u);
+}
+
+// four codes re-rounded, each with its own ratio: one rounding, the products are exact
+__device__ __forceinline__ uint32_t put4(uint32_t w, float r0, float r1, float r2, float r3)
+{
+    const float2 lo = e4m3x2_to_f32x2(w), hi = e4m3x2_to_f32x2(w >> 16);
+    return f32x2_to_e4m3x2(lo.x * r0, lo.y * r1) | f32x2_to_e4m3x2(hi.x * r2, hi.y * r3) << 16;
+}
+
+// A code that is not 0 has a ratio below 2^18, for the new scale keeps it within 448; a
+// zero's ratio may be anything, infinite even.
+__device__ __forceinline__ float code_ratio(float scale, float inverse) { return fminf(scale * inverse, 1048576.f); }
+
 template <int D>
-__global__ void __launch_bounds__(2 * D)
+__global__ void __launch_bounds__(D)
 cache_move_kernel(const CacheCall c, int keep, int blocks, const int32_t *__restrict__ new_pages,
                   const int32_t *__restrict__ kept)
 {
-    constexpr int NT = 2 * D, LD = 68;  // bytes of a padded row
-    __shared__ __align__(16) uint8_t src[D * LD], dst[D * LD];
-    __shared__ int tok_page[kPage], tok_slot[kPage];
-    __shared__ float tok_ks[kPage], tok_vs[kPage];
-    __shared__ uint32_t smax[2][D / 16];
+    constexpr int LD = 17;  // words of a row: byte reads of 32 rows meet no bank conflict
+    __shared__ uint32_t src[D * LD], dst[D * LD];
+    __shared__ __align__(16) int tok_page[kPage], tok_slot[kPage];
+    __shared__ __align__(16) float tok_ks[kPage], tok_vs[kPage];
+    __shared__ uint32_t smax[2][D / 32];
     const int h = (int)(blockIdx.x % (unsigned)c.H);
     const int j = (int)(blockIdx.x / (unsigned)c.H % (unsigned)blocks);
     const int b = (int)(blockIdx.x / ((unsigned)c.H * (unsigned)blocks));
+    const int tid = threadIdx.x, lane = tid & 31;
     const CacheSeq s = cache_seq(c, b);
     if (s.len <= keep)
         return;
-    const int tid = threadIdx.x;
     const int count = min(keep - j * kPage, kPage);
     const int to = table_page(new_pages, c, b, j);
     if (to < 0) {
@@ -195,92 +225,106 @@ cache_move_kernel(const CacheCall c, int keep, int blocks, const int32_t *__rest
             atomicOr(&c.hdr->flag, FLAG_CACHE_PAGE);
         return;
     }
-    if (tid < kPage) {
+    for (int u = tid; u < kPage; u += D) {
         int page = -1, slot = 0;
-        if (tid < count) {
-            const int i = kept[(int64_t)b * keep + j * kPage + tid];
+        if (u < count) {
+            const int i = kept[(int64_t)b * keep + j * kPage + u];
             page = table_page(c.table, c, b, i / kPage);
             slot = i % kPage;
         }
-        tok_page[tid] = page;
-        tok_slot[tid] = slot;
-        tok_ks[tid] = page < 0 ? 0.f : c.k_scale[(int64_t)page * c.H + h];
-        tok_vs[tid] = page < 0 ? 0.f : c.v_scale[(int64_t)page * c.H + h];
-        if (h == 0 && tid < count && page >= 0) {
-            const int64_t from = (int64_t)page * kPage + slot, at = (int64_t)to * kPage + tid;
+        tok_page[u] = page;
+        tok_slot[u] = slot;
+        tok_ks[u] = page < 0 ? 0.f : c.k_scale[(int64_t)page * c.H + h];
+        tok_vs[u] = page < 0 ? 0.f : c.v_scale[(int64_t)page * c.H + h];
+        if (h == 0 && page >= 0) {
+            const int64_t from = (int64_t)page * kPage + slot, at = (int64_t)to * kPage + u;
             c.timestamps[at] = c.timestamps[from];
             c.positions[at] = c.positions[from];
             c.weights[at] = c.weights[from];
         }
     }
     __syncthreads();
-    // keys of this thread's 4 tokens x 8 dims
-    const int part = tid % (D / 8), quad = tid / (D / 8), t0 = 4 * quad;
-    uint2 kw[4];
+    // 16 codes each of four of the keys
+    constexpr int PK = D / 16;  // pieces of a key
+    uint4 kw[4];
 #pragma unroll
-    for (int t = 0; t < 4; t++) {
-        const int page = tok_page[t0 + t];
-        kw[t] = page < 0 ? make_uint2(0u, 0u)
-                         : *reinterpret_cast<const uint2 *>(c.k_codes + block_offset<D>(page, c.H, h) +
-                                                            tok_slot[t0 + t] * D + 8 * part);
+    for (int i = 0; i < 4; i++) {
+        const int x = tid + i * D, u = x / PK, page = tok_page[u];
+        kw[i] = page < 0 ? make_uint4(0u, 0u, 0u, 0u)
+                         : *reinterpret_cast<const uint4 *>(c.k_codes + block_offset<D>(page, c.H, h) +
+                                                            tok_slot[u] * D + x % PK * 16);
     }
-    // values: the tokens of one source page are neighbours (kept is ascending)
-    for (int t = 0; t < count;) {
-        const int page = tok_page[t];
-        int t1 = t + 1;
-        while (t1 < count && tok_page[t1] == page)
-            t1++;
-        if (page >= 0) {
-            const uint8_t *vb = c.v_codes + block_offset<D>(page, c.H, h);
-            for (int i = tid; i < D * 4; i += NT) {
-                const uint4 w = *reinterpret_cast<const uint4 *>(vb + 16 * i);
-                uint32_t *p = reinterpret_cast<uint32_t *>(src + (i >> 2) * LD + (i & 3) * 16);
-                p[0] = w.x, p[1] = w.y, p[2] = w.z, p[3] = w.w;
+    // values: runs of tokens of one source page (kept is ascending)
+    uint64_t starts = 0;
+    {
+        const int u0 = lane, u1 = lane + 32;
+        const uint32_t lo = __ballot_sync(0xffffffffu, u0 < count && (u0 == 0 || tok_page[u0] != tok_page[u0 - 1]));
+        const uint32_t hi = __ballot_sync(0xffffffffu, u1 < count && tok_page[u1] != tok_page[u1 - 1]);
+        starts = (uint64_t)hi << 32 | lo;
+    }
+    uint4 v[4];
+    auto fetch = [&](int u) {  // this dim's row of token u's page
+        const int page = tok_page[u];
+        const uint8_t *p = c.v_codes + block_offset<D>(page < 0 ? 0 : page, c.H, h) + tid * kPage;
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            v[i] = page < 0 ? make_uint4(0u, 0u, 0u, 0u) : *reinterpret_cast<const uint4 *>(p + 16 * i);
+    };
+    uint32_t *srow = src + tid * LD, *drow = dst + tid * LD;
+    const uint8_t *sbytes = reinterpret_cast<const uint8_t *>(srow);
+    uint8_t *dbytes = reinterpret_cast<uint8_t *>(drow);
+    uint32_t mk = 0, mv = 0;
+    auto magnitude = [](uint32_t code, float scale) {
+        return __float_as_uint(e4m3x2_to_f32x2(code).x * scale) & 0x7fffffffu;
+    };
+#pragma unroll
+    for (int i = 0; i < 16; i++)
+        drow[i] = 0u;
+    fetch(0);
+    for (int u = 0; u < count;) {
+        starts &= starts - 1;
+        const int end = starts ? __ffsll((long long)starts) - 1 : count;
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            srow[4 * i] = v[i].x;
+            srow[4 * i + 1] = v[i].y;
+            srow[4 * i + 2] = v[i].z;
+            srow[4 * i + 3] = v[i].w;
+        }
+        if (end < count)
+            fetch(end);
+        uint32_t top = 0;
+        const float vs = tok_vs[u];
+        while (u < end) {
+            if ((u & 3) == 0 && u + 4 <= end) {
+                const int4 sl = *reinterpret_cast<const int4 *>(&tok_slot[u]);
+                const uint32_t x = (uint32_t)sbytes[sl.x] | (uint32_t)sbytes[sl.y] << 8 | (uint32_t)sbytes[sl.z] << 16 |
+                                   (uint32_t)sbytes[sl.w] << 24;
+                drow[u >> 2] = x;
+                top = max(top, max_code(x));
+                u += 4;
+            } else {
+                const uint32_t x = sbytes[tok_slot[u]];
+                dbytes[u++] = (uint8_t)x;
+                top = max(top, x & 127u);
             }
         }
-        __syncthreads();
-        const int d = tid % D;
-        for (int u = t + tid / D; u < t1; u += 2)
-            dst[d * LD + u] = page < 0 ? 0 : src[d * LD + tok_slot[u]];
-        __syncthreads();
-        t = t1;
+        mv = max(mv, magnitude(top, vs));
     }
-    for (int u = count + tid / D; u < kPage; u += 2)
-        dst[(tid % D) * LD + u] = 0;
-    __syncthreads();
-    uint32_t vw[8], mk = 0, mv = 0;
 #pragma unroll
-    for (int e = 0; e < 8; e++)
-        vw[e] = *reinterpret_cast<const uint32_t *>(dst + (8 * part + e) * LD + t0);
-    float ksc[4], vsc[4];
-#pragma unroll
-    for (int t = 0; t < 4; t++) {
-        ksc[t] = tok_ks[t0 + t];
-        vsc[t] = tok_vs[t0 + t];
-    }
-    auto mag = [](float x) { return __float_as_uint(x) & 0x7fffffffu; };
-#pragma unroll
-    for (int t = 0; t < 4; t++)
-#pragma unroll
-        for (int e = 0; e < 4; e++) {
-            const float2 f = e4m3x2_to_f32x2((e < 2 ? kw[t].x : kw[t].y) >> (16 * (e & 1)));
-            mk = max(mk, max(mag(f.x * ksc[t]), mag(f.y * ksc[t])));
-        }
-#pragma unroll
-    for (int e = 0; e < 8; e++) {
-        const float2 lo = e4m3x2_to_f32x2(vw[e]), hi = e4m3x2_to_f32x2(vw[e] >> 16);
-        mv = max(mv, max(max(mag(lo.x * vsc[0]), mag(lo.y * vsc[1])), max(mag(hi.x * vsc[2]), mag(hi.y * vsc[3]))));
+    for (int i = 0; i < 4; i++) {
+        const uint32_t top = max(max(max_code(kw[i].x), max_code(kw[i].y)), max(max_code(kw[i].z), max_code(kw[i].w)));
+        mk = max(mk, magnitude(top, tok_ks[(tid + i * D) / PK]));
     }
     mk = __reduce_max_sync(0xffffffffu, mk);
     mv = __reduce_max_sync(0xffffffffu, mv);
-    if ((tid & 31) == 0) {
+    if (lane == 0) {
         smax[0][tid >> 5] = mk;
         smax[1][tid >> 5] = mv;
     }
     __syncthreads();
-    mk = mv = 0;
 #pragma unroll
-    for (int w = 0; w < D / 16; w++) {
+    for (int w = 0; w < D / 32; w++) {
         mk = max(mk, smax[0][w]);
         mv = max(mv, smax[1][w]);
     }
@@ -291,50 +335,44 @@ cache_move_kernel(const CacheCall c, int keep, int blocks, const int32_t *__rest
         c.v_scale[(int64_t)to * c.H + h] = vs;
     }
     uint8_t *kc = c.k_codes + block_offset<D>(to, c.H, h);
-    uint8_t *vc = c.v_codes + block_offset<D>(to, c.H, h);
-    // re-rounded at the new scale: two exact products, so one rounding
-    auto put2 = [](uint32_t codes, float r0, float r1) {
-        const float2 f = e4m3x2_to_f32x2(codes);
-        return f32x2_to_e4m3x2(f.x * r0, f.y * r1);
-    };
 #pragma unroll
-    for (int t = 0; t < 4; t++) {
-        if (t0 + t >= count)
+    for (int i = 0; i < 4; i++) {
+        const int x = tid + i * D, u = x / PK;
+        if (u >= count)
             continue;
-        const float r = ksc[t] * ki;
-        *reinterpret_cast<uint2 *>(kc + (t0 + t) * D + 8 * part) =
-            make_uint2(put2(kw[t].x, r, r) | (put2(kw[t].x >> 16, r, r) << 16),
-                       put2(kw[t].y, r, r) | (put2(kw[t].y >> 16, r, r) << 16));
+        const float r = code_ratio(tok_ks[u], ki);
+        *reinterpret_cast<uint4 *>(kc + u * D + x % PK * 16) =
+            make_uint4(put4(kw[i].x, r, r, r, r), put4(kw[i].y, r, r, r, r), put4(kw[i].z, r, r, r, r),
+                       put4(kw[i].w, r, r, r, r));
     }
+    uint8_t *vc = c.v_codes + block_offset<D>(to, c.H, h) + tid * kPage;
 #pragma unroll
-    for (int e = 0; e < 8; e++) {
-        const float r0 = vsc[0] * vi, r1 = vsc[1] * vi, r2 = vsc[2] * vi, r3 = vsc[3] * vi;
-        *reinterpret_cast<uint32_t *>(dst + (8 * part + e) * LD + t0) =
-            put2(vw[e], r0, r1) | (put2(vw[e] >> 16, r2, r3) << 16);
-    }
-    __syncthreads();
-    for (int i = tid; i < D * 4; i += NT) {
-        const int d = i >> 2, q = (i & 3) * 16;
-        const uint32_t *p = reinterpret_cast<const uint32_t *>(dst + d * LD + q);
-        uint4 w = make_uint4(p[0], p[1], p[2], p[3]);
-        uint4 *g = reinterpret_cast<uint4 *>(vc + d * kPage + q);
-        if (q + 16 > count) {  // slots behind the last token keep their bytes
-            const uint4 was = *g;
-            auto mix = [&](uint32_t a, uint32_t o, int base) {
-                const int n = count - base;
-                const uint32_t m = n >= 4 ? 0xffffffffu : n <= 0 ? 0u : (1u << (8 * n)) - 1u;
-                return (a & m) | (o & ~m);
-            };
-            w = make_uint4(mix(w.x, was.x, q), mix(w.y, was.y, q + 4), mix(w.z, was.z, q + 8), mix(w.w, was.w, q + 12));
+    for (int i = 0; i < 4; i++) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            const float4 r = *reinterpret_cast<const float4 *>(&tok_vs[16 * i + 4 * e]);
+            w[e] = put4(drow[4 * i + e], code_ratio(r.x, vi), code_ratio(r.y, vi), code_ratio(r.z, vi), code_ratio(r.w, vi));
         }
-        *g = w;
+        uint4 *g = reinterpret_cast<uint4 *>(vc + 16 * i);
+        if (16 * i + 16 > count) {  // slots behind the last token keep their bytes
+            const uint4 was = *g;
+            const uint32_t old[4] = {was.x, was.y, was.z, was.w};
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                const int n = count - 16 * i - 4 * e;
+                const uint32_t mask = n >= 4 ? 0xffffffffu : n <= 0 ? 0u : (1u << (8 * n)) - 1u;
+                w[e] = (w[e] & mask) | (old[e] & ~mask);
+            }
+        }
+        *g = make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
 
 template <int D>
 void move(const CacheCall &c, int keep, int blocks, const int32_t *new_pages, const int32_t *kept, cudaStream_t stream)
 {
-    cache_move_kernel<D><<<(unsigned)((int64_t)c.B * blocks * c.H), 2 * D, 0, stream>>>(c, keep, blocks, new_pages,
+    cache_move_kernel<D><<<(unsigned)((int64_t)c.B * blocks * c.H), D, 0, stream>>>(c, keep, blocks, new_pages,
                                                                                        kept);
 }
 
@@ -346,8 +384,13 @@ cudaError_t launch_cache_evict(const CacheCall &c, int keep, int first, int rece
 {
     if (c.B == 0)
         return cudaSuccess;
-    cache_select_kernel<<<c.B, kSelThreads, 0, stream>>>(c, keep, first, recent, new_pages, new_table, new_lens, kept,
-                                                         keys, cap);
+    // all keys in the registers of 256 threads, whose barriers are cheap, or of 1024
+    if (c.max_cache_len <= kSelKeys * 256)
+        cache_select_kernel<256><<<c.B, 256, 0, stream>>>(c, keep, first, recent, new_pages, new_table, new_lens, kept,
+                                                          keys, cap);
+    else
+        cache_select_kernel<1024><<<c.B, 1024, 0, stream>>>(c, keep, first, recent, new_pages, new_table, new_lens,
+                                                            kept, keys, cap);
     if (c.max_cache_len > keep) {
         const int blocks = std::min((keep + kPage - 1) / kPage, c.max_pages);
         switch (c.d) {

@@ -347,6 +347,8 @@ EVICT = [
     ([300], 10, 20, 20),
     ([300, 301], 100, 64, 0),
     ([4000], 1024, 4, 256),
+    ([5000, 4097], 4096, 64, 1000),
+    ([40000, 16385], 300, 3, 17),
 ]
 
 
