@@ -1,16 +1,17 @@
 // Eviction from the 8-bit key/value cache by accumulated attention weight.
 //
 // Select (one CTA per sequence): weights become integers that compare as the weights
-// do (NaN 0).  The m-th largest of the unprotected tokens is found bit by bit, each bit
-// one count of the keys at or above a candidate; the first 16,384 keys stay in
-// registers, sixteen a thread, so that a bit costs one barrier.  (Histograms of 8 bits
-// in shared memory took 30 us for 12,288 tokens: equal exponents crowd into few bins.)
-// Ballots and two scans then place the kept indices, ties to the lowest.
+// do (NaN 0), the first 16 a thread in registers.  Histograms in shared memory of 11, 11
+// and 10 bits find the m-th largest of the unprotected tokens; the first digit holds two
+// bits of the fraction, for weights share few exponents and would crowd into few bins
+// (8-bit digits: 30 us for 12,288 tokens; a count per bit: 33 us).  Ballots and two scans
+// then place the kept indices, ties to the lowest.
 //
 // Move (one CTA per new block and head, a thread per dim): keys are gathered as rows of
 // 16-byte pieces.  Values are stored transposed: a thread takes its dim's row of every
 // source page the block draws on, the next page's on its way meanwhile, through a
-// shared-memory row of its own (no barriers), and picks the kept bytes.  The block gets
+// shared-memory row of its own (no barriers wider than a warp), and picks the kept bytes;
+// memory sees the warp's 32 rows as 512-byte accesses.  The block gets
 // its own scale from the largest decoded magnitude.  Bound by HBM: the kept keys and the
 // source pages of the values are read once, the new block written.
 #include <algorithm>
@@ -31,17 +32,6 @@ __device__ __forceinline__ uint32_t weight_key(float w)
 }
 
 constexpr int kSelKeys = 16;  // keys a thread keeps in registers
-
-// sum over the block's threads; `slots`: 32 ints that no earlier call still reads
-template <int kWarps>
-__device__ __forceinline__ int block_sum(int x, int *slots)
-{
-    x = __reduce_add_sync(0xffffffffu, x);
-    if ((threadIdx.x & 31) == 0)
-        slots[threadIdx.x >> 5] = x;
-    __syncthreads();
-    return __reduce_add_sync(0xffffffffu, (threadIdx.x & 31) < kWarps ? slots[threadIdx.x & 31] : 0);
-}
 
 // In place, exclusive prefix sums of counts[0, 16 kWarps); returns the total.
 template <int kWarps>
@@ -74,8 +64,8 @@ cache_select_kernel(const CacheCall c, int keep, int first, int recent, const in
                     int32_t *__restrict__ new_table, int32_t *__restrict__ new_lens, int32_t *__restrict__ kept,
                     uint32_t *__restrict__ keys, int64_t cap)
 {
-    constexpr int kSelWarps = kSelThreads / 32;
-    __shared__ int slots[2][32], counts[kSelKeys * kSelWarps];
+    constexpr int kSelWarps = kSelThreads / 32, kBins = 2048;
+    __shared__ int slots[2][32], counts[kSelKeys * kSelWarps], bins[kBins], found[3];
     const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const CacheSeq s = cache_seq(c, b);
     const int L = s.len;
@@ -113,28 +103,60 @@ cache_select_kernel(const CacheCall c, int keep, int first, int recent, const in
         rest[j] = key_of(j);
     if (bad)
         atomicOr(&c.hdr->flag, FLAG_CACHE_PAGE);
-    // the largest value that at least m open keys reach (0 if m is 0: then nothing is taken)
-    uint32_t at = 0;
-    int turn = 0;
-    auto count_from = [&](uint32_t want) {  // open keys at or above it (want > 0: the closed ones are 0)
-        int n = 0;
+    // prefix: the m-th largest open key, of whose equals the first `ties` are kept; with
+    // `exact`, the digits so far already part exactly m keys from the others
+    uint32_t prefix = 0, mask = 0;
+    int turn = 0, ties = m;
+    bool exact = false;
+    for (int shift = 21, n = kBins; m > 0 && !exact; shift = max(shift - 11, 0)) {
+        for (int i = tid; i < n; i += kSelThreads)
+            bins[i] = 0;
+        __syncthreads();
 #pragma unroll
         for (int i = 0; i < kSelKeys; i++)
-            if (i * kSelThreads < L)
-                n += key[i] >= want;
+            if (open(i * kSelThreads + tid) && (key[i] & mask) == prefix)
+                atomicAdd(&bins[key[i] >> shift & (n - 1)], 1);
         for (int j = kRound + tid; j < L; j += kSelThreads)
-            n += rest[j] >= want;
-        return block_sum<kSelWarps>(n, slots[turn ^= 1]);
-    };
-    for (uint32_t bit = 0x80000000u; bit != 0 && m > 0; bit >>= 1) {
-        const int n = count_from(at | bit);
-        if (n >= m)
-            at |= bit;
-        if (n == m)  // exactly these
+            if (open(j) && (rest[j] & mask) == prefix)
+                atomicAdd(&bins[rest[j] >> shift & (n - 1)], 1);
+        __syncthreads();
+        // from the highest bin down, the one in which the running count reaches `ties`
+        const int per = n / kSelThreads, top = n - 1 - tid * per;
+        int sum = 0;
+        for (int e = 0; e < per; e++)
+            sum += bins[top - e];
+        int inc = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o)
+                inc += y;
+        }
+        int *slot = slots[turn ^= 1];
+        if (lane == 31)
+            slot[warp] = inc;
+        __syncthreads();
+        int run = inc - sum + __reduce_add_sync(0xffffffffu, lane < warp ? slot[lane] : 0);
+        if (run < ties && run + sum >= ties)
+            for (int e = 0; e < per; e++) {
+                const int x = bins[top - e];
+                if (run < ties && run + x >= ties) {
+                    found[0] = top - e;
+                    found[1] = ties - run;
+                    found[2] = x;
+                }
+                run += x;
+            }
+        __syncthreads();
+        prefix |= (uint32_t)found[0] << shift;
+        mask |= (uint32_t)(n - 1) << shift;
+        ties = found[1];
+        exact = found[1] == found[2];
+        if (shift == 0)
             break;
+        n = shift == 21 ? kBins : 1024;  // digits at 21, 10 and 0
+        __syncthreads();
     }
-    const int above = at == 0xffffffffu ? 0 : count_from(at + 1);
-    const int ties = m > 0 ? m - above : 0;  // of the keys equal to `at`, the first ones
     // in rounds of 16 x 1024 tokens: what each warp's 32 tokens hold, scanned
     const uint32_t below = (1u << lane) - 1u;
     int ties_before = 0, out_before = 0;
@@ -147,8 +169,8 @@ cache_select_kernel(const CacheCall c, int keep, int first, int recent, const in
 #pragma unroll
         for (int i = 0; i < kSelKeys; i++) {
             const int j = j0 + i * kSelThreads + tid;
-            const bool is_tie = m > 0 && open(j) && key[i] == at;
-            const bool is_safe = j < L && (!open(j) || (m > 0 && key[i] > at));
+            const bool is_tie = m > 0 && !exact && open(j) && key[i] == prefix;
+            const bool is_safe = j < L && (!open(j) || (m > 0 && (exact ? (key[i] & mask) >= prefix : key[i] > prefix)));
             safe |= (uint32_t)is_safe << i;
             tie |= (uint32_t)is_tie << i;
             const uint32_t votes = __ballot_sync(0xffffffffu, is_tie);
@@ -197,12 +219,25 @@ __device__ __forceinline__ uint32_t put4(uint32_t w, float r0, float r1, float r
     return f32x2_to_e4m3x2(lo.x * r0, lo.y * r1) | f32x2_to_e4m3x2(hi.x * r2, hi.y * r3) << 16;
 }
 
+// the same in 16 bits, for ratios of at most 2^15: a 4-bit significand times a power of
+// two is exact down to f16's last place, 2^-24, far below E4M3's first tie at 2^-10
+__device__ __forceinline__ uint32_t put4h(uint32_t w, __half2 r01, __half2 r23)
+{
+    const uint32_t a = e4m3x2_to_f16x2(w), b = e4m3x2_to_f16x2(w >> 16);
+    const __half2 x = __hmul2(*reinterpret_cast<const __half2 *>(&a), r01);
+    const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&b), r23);
+    unsigned short lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(lo) : "r"(*reinterpret_cast<const uint32_t *>(&x)));
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(hi) : "r"(*reinterpret_cast<const uint32_t *>(&y)));
+    return (uint32_t)lo | (uint32_t)hi << 16;
+}
+
 // A code that is not 0 has a ratio below 2^18, for the new scale keeps it within 448; a
 // zero's ratio may be anything, infinite even.
 __device__ __forceinline__ float code_ratio(float scale, float inverse) { return fminf(scale * inverse, 1048576.f); }
 
 template <int D>
-__global__ void __launch_bounds__(D)
+__global__ void __launch_bounds__(D, D == 32 ? 16 : 1280 / D)
 cache_move_kernel(const CacheCall c, int keep, int blocks, const int32_t *__restrict__ new_pages,
                   const int32_t *__restrict__ kept)
 {
@@ -211,6 +246,7 @@ cache_move_kernel(const CacheCall c, int keep, int blocks, const int32_t *__rest
     __shared__ __align__(16) int tok_page[kPage], tok_slot[kPage];
     __shared__ __align__(16) float tok_ks[kPage], tok_vs[kPage];
     __shared__ uint32_t smax[2][D / 32];
+    __shared__ __align__(8) __half tok_rk[kPage], tok_rv[kPage];  // ratios
     const int h = (int)(blockIdx.x % (unsigned)c.H);
     const int j = (int)(blockIdx.x / (unsigned)c.H % (unsigned)blocks);
     const int b = (int)(blockIdx.x / ((unsigned)c.H * (unsigned)blocks));
@@ -263,12 +299,14 @@ cache_move_kernel(const CacheCall c, int keep, int blocks, const int32_t *__rest
         starts = (uint64_t)hi << 32 | lo;
     }
     uint4 v[4];
-    auto fetch = [&](int u) {  // this dim's row of token u's page
+    // the warp's 32 rows of a block: piece i of a lane is bytes [16 (lane % 4), + 16) of row 8 i + lane / 4
+    const int warp_row = tid & ~31, my_row = lane >> 2, my_piece = lane & 3;
+    auto fetch = [&](int u) {  // of token u's page
         const int page = tok_page[u];
-        const uint8_t *p = c.v_codes + block_offset<D>(page < 0 ? 0 : page, c.H, h) + tid * kPage;
+        const uint8_t *p = c.v_codes + block_offset<D>(page < 0 ? 0 : page, c.H, h) + warp_row * kPage + 16 * lane;
 #pragma unroll
         for (int i = 0; i < 4; i++)
-            v[i] = page < 0 ? make_uint4(0u, 0u, 0u, 0u) : *reinterpret_cast<const uint4 *>(p + 16 * i);
+            v[i] = page < 0 ? make_uint4(0u, 0u, 0u, 0u) : *reinterpret_cast<const uint4 *>(p + 512 * i);
     };
     uint32_t *srow = src + tid * LD, *drow = dst + tid * LD;
     const uint8_t *sbytes = reinterpret_cast<const uint8_t *>(srow);
@@ -284,13 +322,13 @@ cache_move_kernel(const CacheCall c, int keep, int blocks, const int32_t *__rest
     for (int u = 0; u < count;) {
         starts &= starts - 1;
         const int end = starts ? __ffsll((long long)starts) - 1 : count;
+        __syncwarp();
 #pragma unroll
         for (int i = 0; i < 4; i++) {
-            srow[4 * i] = v[i].x;
-            srow[4 * i + 1] = v[i].y;
-            srow[4 * i + 2] = v[i].z;
-            srow[4 * i + 3] = v[i].w;
+            uint32_t *x = src + (warp_row + 8 * i + my_row) * LD + 4 * my_piece;
+            x[0] = v[i].x, x[1] = v[i].y, x[2] = v[i].z, x[3] = v[i].w;
         }
+        __syncwarp();
         if (end < count)
             fetch(end);
         uint32_t top = 0;
@@ -334,33 +372,52 @@ cache_move_kernel(const CacheCall c, int keep, int blocks, const int32_t *__rest
         c.k_scale[(int64_t)to * c.H + h] = ks;
         c.v_scale[(int64_t)to * c.H + h] = vs;
     }
+    bool large = false;  // a ratio that f16 does not hold
+    for (int u = tid; u < count; u += D) {
+        const float rk = code_ratio(tok_ks[u], ki), rv = code_ratio(tok_vs[u], vi);
+        large |= rk > 32768.f || rv > 32768.f;
+        tok_rk[u] = __float2half_rn(rk);
+        tok_rv[u] = __float2half_rn(rv);
+    }
+    large = __syncthreads_or(large);
     uint8_t *kc = c.k_codes + block_offset<D>(to, c.H, h);
 #pragma unroll
     for (int i = 0; i < 4; i++) {
         const int x = tid + i * D, u = x / PK;
         if (u >= count)
             continue;
+        uint32_t w[4] = {kw[i].x, kw[i].y, kw[i].z, kw[i].w};
         const float r = code_ratio(tok_ks[u], ki);
-        *reinterpret_cast<uint4 *>(kc + u * D + x % PK * 16) =
-            make_uint4(put4(kw[i].x, r, r, r, r), put4(kw[i].y, r, r, r, r), put4(kw[i].z, r, r, r, r),
-                       put4(kw[i].w, r, r, r, r));
+        const __half2 rh = __half2half2(tok_rk[u]);
+#pragma unroll
+        for (int e = 0; e < 4; e++)
+            w[e] = large ? put4(w[e], r, r, r, r) : put4h(w[e], rh, rh);
+        *reinterpret_cast<uint4 *>(kc + u * D + x % PK * 16) = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    uint8_t *vc = c.v_codes + block_offset<D>(to, c.H, h) + tid * kPage;
+#pragma unroll
+    for (int i = 0; i < 16; i++) {
+        const int u = 4 * i;
+        if (large) {
+            const float4 r = *reinterpret_cast<const float4 *>(&tok_vs[u]);
+            drow[i] = put4(drow[i], code_ratio(r.x, vi), code_ratio(r.y, vi), code_ratio(r.z, vi), code_ratio(r.w, vi));
+        } else {
+            const __half2 *r = reinterpret_cast<const __half2 *>(&tok_rv[u]);
+            drow[i] = put4h(drow[i], r[0], r[1]);
+        }
+    }
+    __syncwarp();
+    uint8_t *vc = c.v_codes + block_offset<D>(to, c.H, h) + warp_row * kPage + 16 * lane;
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-        uint32_t w[4];
-#pragma unroll
-        for (int e = 0; e < 4; e++) {
-            const float4 r = *reinterpret_cast<const float4 *>(&tok_vs[16 * i + 4 * e]);
-            w[e] = put4(drow[4 * i + e], code_ratio(r.x, vi), code_ratio(r.y, vi), code_ratio(r.z, vi), code_ratio(r.w, vi));
-        }
-        uint4 *g = reinterpret_cast<uint4 *>(vc + 16 * i);
-        if (16 * i + 16 > count) {  // slots behind the last token keep their bytes
+        const uint32_t *x = dst + (warp_row + 8 * i + my_row) * LD + 4 * my_piece;
+        uint32_t w[4] = {x[0], x[1], x[2], x[3]};
+        uint4 *g = reinterpret_cast<uint4 *>(vc + 512 * i);
+        if (16 * my_piece + 16 > count) {  // slots behind the last token keep their bytes
             const uint4 was = *g;
             const uint32_t old[4] = {was.x, was.y, was.z, was.w};
 #pragma unroll
             for (int e = 0; e < 4; e++) {
-                const int n = count - 16 * i - 4 * e;
+                const int n = count - 16 * my_piece - 4 * e;
                 const uint32_t mask = n >= 4 ? 0xffffffffu : n <= 0 ? 0u : (1u << (8 * n)) - 1u;
                 w[e] = (w[e] & mask) | (old[e] & ~mask);
             }
