@@ -9,7 +9,7 @@
 // (Loaded straight into registers, the blocks left two warps a scheduler: 4.1 TB/s.)
 // Keys and dims are the rows of the 16-bit matrix instructions, the queries their eight
 // columns, so that a page of d = 128 takes 64 of them for eight queries (with queries as
-// the sixteen rows it took 128, and those were the bound: 200 us where this takes 1XX).
+// the sixteen rows it took 128, and those were the bound: 200 us where this takes 160).
 //   S^T = K Q^T, O^T = V^T P^T
 // A page's layouts (keys [64][d], values [d][64]) are row-major A operands, and the order
 // of the contracted index is free, so a lane's 16-byte read is four instructions' operand:
@@ -195,16 +195,34 @@ cache_attn_rows_kernel(const CacheAttnArgs a)
             continue;
         }
         const float ks = c.k_scale[(int64_t)page * c.H + h], vs = c.v_scale[(int64_t)page * c.H + h];
-        // biases of keys lane and lane + 32 for every row
+        // biases of keys lane and lane + 32 for every row, the table reads of four rows in flight
         __syncwarp();
+        int pj[2];
+        int64_t tj[2];
 #pragma unroll
         for (int e = 0; e < 2; e++) {
             const int64_t at = (int64_t)page * kPage + lane + 32 * e;
-            const int pj = c.positions[at];
-            const int64_t tj = c.timestamps[at];
-            for (int r = 0; r < rows; r++)
-                bias[(lane + 32 * e) * kBiasLd + r] =
-                    rp[pos_index(row_pi[r], pj, a.pos_lo, a.pos_hi)] + rt_[time_bucket(row_ti[r], tj, a.nb)];
+            pj[e] = c.positions[at];
+            tj[e] = c.timestamps[at];
+        }
+        if (rows == 1) {
+#pragma unroll
+            for (int e = 0; e < 2; e++)
+                bias[(lane + 32 * e) * kBiasLd] =
+                    rp[pos_index(row_pi[0], pj[e], a.pos_lo, a.pos_hi)] + rt_[time_bucket(row_ti[0], tj[e], a.nb)];
+        } else {
+#pragma unroll 1
+            for (int r = 0; r < rows; r += 4) {  // rows behind the last repeat it
+                float bp[8], bt[8];
+#pragma unroll
+                for (int x = 0; x < 8; x++) {
+                    bp[x] = rp[pos_index(row_pi[r + (x >> 1)], pj[x & 1], a.pos_lo, a.pos_hi)];
+                    bt[x] = rt_[time_bucket(row_ti[r + (x >> 1)], tj[x & 1], a.nb)];
+                }
+#pragma unroll
+                for (int x = 0; x < 8; x++)
+                    bias[(lane + 32 * (x & 1)) * kBiasLd + r + (x >> 1)] = bp[x] + bt[x];
+            }
         }
         __syncwarp();
         if (!(ok = __all_sync(0xffffffffu, mbar_wait(kbar, loads & 1, &abort_flag, c.hdr))))
