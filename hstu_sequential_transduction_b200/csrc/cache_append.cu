@@ -5,7 +5,9 @@
 // 2^e with amax <= 448 2^e, code = E4M3(x 2^-e); a partly filled block keeps the
 // larger of its old scale and the new one, and its older codes are shifted to it.
 //
-// Bound by HBM: each k and v element is read once and its code written once.
+// Bound by HBM: each k and v element is read once and its code written once (98,000
+// tokens of 4 heads, d = 128: 86 us, 3.5 TB/s; with the rows widened to floats before
+// the reduction, two CTAs an SM, 127 us).
 // One CTA per (sequence, block, head), 2 D threads: a thread takes 4 tokens x 8
 // dims of K and of V, all eight 16-byte (bf16) loads in flight before the one
 // reduction.  Keys leave as 8 bytes per token (16 lanes fill a 128-byte row).

@@ -13,21 +13,24 @@
 // Keys stay codes: a query is split into two E4M3 parts, q = (q1 + q2) 2^e, q1 the
 // nearest code, q2 the nearest code of what is left.  Two four-bit significands hold
 // bf16's eight exactly; below 2^-6 of the scale the parts go subnormal, so an element
-// is held to 2^-18.8 of the largest magnitude of its scale.  The scale is shared by
-// the 32 rows of a chunk if no row's largest is 2^3 or more below theirs, else each
-// row has its own.  E4M3 runs at twice the bf16 rate, so both parts cost what one
-// bf16 product would, and no key is ever converted.
+// is held to 2^-17.8 of the largest magnitude under its scale.  A scale is shared by the
+// 16 rows of a chunk if no row's largest is 2^3 or more below theirs, else each row has
+// its own.  E4M3 runs at twice the bf16 rate, so both parts cost what one bf16 product
+// would, and no key is ever converted.
 // Values become bf16 (exactly, with their page's scale) in registers on the way from
 // memory to TMEM; P is rounded to bf16 once.
 //
-// Bound: per 128 x 128 tile at d = 128, 1024 cycles of the tensor pipe, of MUFU (one
-// tanh per pair) and of shared-memory bandwidth (512 S^T operands, 256 P^T stores,
-// 256 P^T reads) alike; V^T as a TMEM operand is what keeps the last at 1024.
-//
-// Warp roles (512 threads): warp 0 loads the codes (TMA); warp 1 owns TMEM and issues
-// the MMAs (2 and 3 idle); warps 4-19, in four groups,
-// write P^T; warps 12-15 split queries and convert values.
-// TMEM columns: S^T [0, 128) and [128, 256), O^T [256, 384), V^T [384, 448), [448, 512).
+// Per 128 x 128 tile at d = 128 the tensor pipe, MUFU (one tanh per pair) and shared
+// memory need 1024 cycles each; V^T as a TMEM operand is what keeps the last there.  The
+// kernel takes ~2,200: it is bound by its issue slots (~8,000 warp instructions a tile,
+// half of them the math).  So what a tile needs besides is spread over many warps:
+// Warp roles (896 threads): 0 loads the codes (TMA); 1 issues S^T and owns TMEM; 2 issues
+// O^T (3 idle); 4-19, four groups, take 64 columns of a tile in turn from S^T to P^T,
+// each with a buffer of S^T and one of P^T; 20-27, two groups, take every other tile's
+// keys (bias, scale) and values (conversion), and together split the queries.
+// (16 users x 512 candidates over 2048 tokens, 2 heads: 38 us; one conversion group 43,
+// the keys' data fetched by the epilogue warps 45, two epilogue groups of 128 columns 48.)
+// TMEM columns: S^T 4 x 64, O^T [256, 384), V^T [384, 448), [448, 512).
 //
 // Work: all (sequence, head, query tile) units' key tiles in one line, cut into equal
 // runs, one per CTA.  A unit inside one run is written to `out`; a cut unit's pieces

@@ -459,6 +459,11 @@ class HstuCache:
         self.device = k_codes.device
         self._structs = {}
 
+    def __setattr__(self, name, value):
+        if hasattr(self, "_structs"):  # the C structs hold the tensors' addresses
+            raise AttributeError("a cache keeps its tensors; make another HstuCache")
+        object.__setattr__(self, name, value)
+
     @classmethod
     def empty(cls, num_pages: int, num_heads: int, head_dim: int, device, weights: bool = True) -> "HstuCache":
         """A cache of num_pages pages, all zero."""
@@ -570,8 +575,9 @@ def hstu_cache_append(k, v, cache: HstuCache, block_table, cache_lens, seq_pos, 
     seq_pos None means cache_lens (nothing was evicted before)."""
     table = _cache_table(cache, block_table, "block_table")
     B, cols = block_table.shape
-    lens, pos, nt = (_cache_ints(cache, B, t, n) for t, n in ((cache_lens, "cache_lens"), (seq_pos, "seq_pos"),
-                                                              (num_targets, "num_targets")))
+    lens = _cache_ints(cache, B, cache_lens, "cache_lens")
+    pos = _cache_ints(cache, B, seq_pos, "seq_pos")
+    nt = _cache_ints(cache, B, num_targets, "num_targets")
     sk, sv = _cache_rows(cache, "k", k), _cache_rows(cache, "v", v)
     if v.dtype != k.dtype or v.shape != k.shape:
         raise ValueError("k and v must have one type and shape")
@@ -582,17 +588,17 @@ def hstu_cache_append(k, v, cache: HstuCache, block_table, cache_lens, seq_pos, 
     if new_pos is None:
         new_pos = torch.empty_like(cache_lens)
     workspace = _cache_workspace(cache, workspace, 256)
-    _cache_call(cache, "hstu_cache_append", stream, cache.struct(cols), _dtype_code(k), B, max_seq_len, T, k.data_ptr(), sk,
+    _cache_call(cache, "hstu_cache_append", stream, cache.struct(cols), _dtype_code(k), B, int(max_seq_len), T, k.data_ptr(), sk,
                 v.data_ptr(), sv, off, ts, nt, table, lens, pos, _cache_ints(cache, B, new_lens, "new_lens"),
                 _cache_ints(cache, B, new_pos, "new_pos"), workspace.data_ptr(), workspace.numel())
     return new_lens, new_pos
 
 
 def _cache_attn_desc(q, block_table, rab_pos, rab_time, max_seq_len, inv_n, pos_lo, pos_hi, cand_own_index):
-    nb, per_head = _tables(rab_pos, rab_time, q.shape[1], pos_lo, pos_hi)
-    return make_attn_desc(block_table.shape[0], max_seq_len, q.shape[0], q.shape[1], q.shape[2], q.shape[2],
-                          _dtype_code(q), inv_n, pos_lo, pos_hi, nb, cand_own_index=cand_own_index,
-                          per_head_tables=per_head)
+    T, H, d = q.shape
+    nb, per_head = _tables(rab_pos, rab_time, H, pos_lo, pos_hi)
+    return hstu_attn_desc(block_table.shape[0], int(max_seq_len), T, H, d, d, _dtype_code(q), inv_n, int(pos_lo),
+                          int(pos_hi), nb, 0, 0, 0, 0, bool(cand_own_index), per_head)
 
 
 def hstu_cache_attn_workspace_size(q, cache: HstuCache, block_table, rab_pos, rab_time, *, max_seq_len: int,
@@ -601,7 +607,7 @@ def hstu_cache_attn_workspace_size(q, cache: HstuCache, block_table, rab_pos, ra
     desc = _cache_attn_desc(q, block_table, rab_pos, rab_time, max_seq_len, inv_n, pos_lo, pos_hi, cand_own_index)
     n = ctypes.c_size_t(0)
     _check("hstu_cache_attn_workspace_size", load_library().hstu_cache_attn_workspace_size(
-        ctypes.byref(desc), cache.struct(block_table.shape[1]), max_cache_len, int(weights), ctypes.byref(n)))
+        ctypes.byref(desc), cache.struct(block_table.shape[1]), int(max_cache_len), int(weights), ctypes.byref(n)))
     return n.value
 
 
@@ -615,8 +621,9 @@ def hstu_cache_attn_fwd(q, cache: HstuCache, block_table, cache_lens, seq_pos, s
     may be cache.weights."""
     table = _cache_table(cache, block_table, "block_table")
     B, cols = block_table.shape
-    lens, pos, nt = (_cache_ints(cache, B, t, n) for t, n in ((cache_lens, "cache_lens"), (seq_pos, "seq_pos"),
-                                                              (num_targets, "num_targets")))
+    lens = _cache_ints(cache, B, cache_lens, "cache_lens")
+    pos = _cache_ints(cache, B, seq_pos, "seq_pos")
+    nt = _cache_ints(cache, B, num_targets, "num_targets")
     sq = _cache_rows(cache, "q", q)
     off, ts = _cache_tokens(cache, B, q.shape[0], seq_offsets, timestamps)
     rp = _on(cache.device, rab_pos, "rab_pos", torch.float32)
@@ -635,10 +642,10 @@ def hstu_cache_attn_fwd(q, cache: HstuCache, block_table, cache_lens, seq_pos, s
         n = ctypes.c_size_t(0)
         with torch.cuda.device(cache.device):
             _check("hstu_cache_attn_workspace_size", load_library().hstu_cache_attn_workspace_size(
-                desc, pool, max_cache_len, int(weights_out is not None), ctypes.byref(n)))
+                desc, pool, int(max_cache_len), int(weights_out is not None), ctypes.byref(n)))
         workspace = alloc_workspace(n.value, cache.device)
     _same_device(workspace, "workspace", cache.device)
-    _cache_call(cache, "hstu_cache_attn_fwd", stream, desc, pool, max_cache_len, q.data_ptr(), sq, off, ts, nt, rp, rt,
+    _cache_call(cache, "hstu_cache_attn_fwd", stream, desc, pool, int(max_cache_len), q.data_ptr(), sq, off, ts, nt, rp, rt,
                 table, lens, pos, _on(cache.device, addend, "addend", q.dtype),
                 _on(cache.device, weights_out, "weights_out", torch.float32), _on(cache.device, out, "out", q.dtype),
                 workspace.data_ptr(), workspace.numel())
@@ -649,7 +656,7 @@ def hstu_cache_evict_workspace_size(cache: HstuCache, block_table, *, keep: int,
                                     recent: int = 0) -> int:
     n = ctypes.c_size_t(0)
     _check("hstu_cache_evict_workspace_size", load_library().hstu_cache_evict_workspace_size(
-        cache.struct(block_table.shape[1]), block_table.shape[0], max_cache_len, keep, ctypes.byref(n)))
+        cache.struct(block_table.shape[1]), block_table.shape[0], int(max_cache_len), int(keep), ctypes.byref(n)))
     return n.value
 
 
@@ -661,6 +668,7 @@ def hstu_cache_evict(cache: HstuCache, block_table, cache_lens, new_pages, *, ke
     of new_pages [B, max_pages].  Returns (new_table, new_lens, kept [B, keep])."""
     table = _cache_table(cache, block_table, "block_table")
     B, cols = block_table.shape
+    keep = int(keep)
     if cache.weights is None:
         raise ValueError("eviction needs the cache's weights")
     if new_table is None:
@@ -675,7 +683,7 @@ def hstu_cache_evict(cache: HstuCache, block_table, cache_lens, new_pages, *, ke
         workspace = alloc_workspace(hstu_cache_evict_workspace_size(cache, block_table, keep=keep,
                                                                     max_cache_len=max_cache_len), cache.device)
     _same_device(workspace, "workspace", cache.device)
-    _cache_call(cache, "hstu_cache_evict", stream, cache.struct(cols), B, max_cache_len, keep, first, recent, table,
+    _cache_call(cache, "hstu_cache_evict", stream, cache.struct(cols), B, int(max_cache_len), keep, int(first), int(recent), table,
                 _cache_ints(cache, B, cache_lens, "cache_lens"),
                 _cache_table(cache, new_pages, "new_pages", block_table.shape),
                 _cache_table(cache, new_table, "new_table", block_table.shape),

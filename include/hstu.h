@@ -312,7 +312,8 @@ hstu_status hstu_gemm_e4m3(const void *codes, const float *scales, int64_t M, in
  * finite (the block's values are then all NaN).  Powers of two divide exactly,
  * so a code is the value's one rounding to E4M3 (nearest even), and a block
  * whose scale grows shifts its older codes (rounding again only those that
- * leave E4M3's normal range).
+ * leave E4M3's normal range).  A pool that was filled in another way needs scales
+ * that are powers of two, 0 or NaN, too.
  *
  * Device checks add two bits to those of hstu_check_device_flag:
  * 64 = cache_lens outside [0, max_cache_len] or the table's room, or tokens
@@ -322,7 +323,7 @@ hstu_status hstu_gemm_e4m3(const void *codes, const float *scales, int64_t M, in
 #define HSTU_CACHE_PAGE 64
 
 typedef struct {
-    int32_t num_pages;  /* pages of the pool */
+    int32_t num_pages;  /* pages of the pool, >= 1 */
     int32_t num_heads;  /* H */
     int32_t head_dim;   /* d */
     int32_t max_pages;  /* columns of a block table */
@@ -362,12 +363,13 @@ hstu_status hstu_cache_attn_workspace_size(const hstu_attn_desc *desc, const hst
  * Attention of a call's tokens over their sequences' whole caches:
  *   s_ij  = q_i . k_j + rab_pos[p_i - p_j] + rab_time[bucket(t_i - t_j)]
  *   out_i = inv_n * sum_j SiLU(s_ij) v_j + addend_i
- *   weights_out_j = weights_j + inv_n * sum over heads and i of |SiLU(s_ij)|
+ *   weights_out_j = weights_j + |inv_n| * sum over heads and i of |SiLU(s_ij)|
  * j runs over the cache_lens[b] cached tokens of i's sequence, all of them
  * visible; p_j and t_j are the cached ones, p_i = seq_pos[b] + i for history
- * tokens and seq_pos[b] + L_b - n_t (+ own index with cand_positions) for
- * candidates.  Biases, clamps and tables as in hstu_attn_fwd.  A sequence with
- * an empty cache gets its addend, or zeros.
+ * tokens and seq_pos[b] + L_b - n_t for candidates (seq_pos[b] + i for them
+ * too with cand_positions = 1).  Biases, clamps and tables as in hstu_attn_fwd.  A sequence with
+ * an empty cache gets its addend, or zeros; the rows of a dropped one and rows
+ * behind the last sequence are left as they were.
  *   desc       the call's tokens; fp8_qk, debug_checks and the windows must be 0
  *   max_cache_len >= every cache_lens[b]; sizes the launch and the workspace
  *   q          [T, H, d], rows q_stride elements apart, 16-byte aligned
@@ -376,8 +378,12 @@ hstu_status hstu_cache_attn_workspace_size(const hstu_attn_desc *desc, const hst
  *              starts from 0 where that is NULL.  Only the cached tokens of the
  *              call's sequences are written; with weights_out these sequences
  *              must not share pages.
- * float32 q is computed to float32 accuracy; for bf16 q, products are exact and
- * sums float32, and P is rounded to 16 bits before P V.
+ * float32 q is computed to float32 accuracy.  For bf16 q sums are float32, and
+ *   max_seq_len <= 64: an element of q is held to 2^-39 of its row's largest, P is
+ *     rounded to 11 bits;
+ *   above: q is held to 2^-14 of its row's largest at worst (two E4M3 parts under
+ *     one scale for rows of similar size), P is rounded to bf16.  num_pages * H *
+ *     max(64, d) must stay below 2^31 (HSTU_ERR_UNSUPPORTED).
  */
 hstu_status hstu_cache_attn_fwd(const hstu_attn_desc *desc, const hstu_cache *cache, int32_t max_cache_len,
                                 const void *q, int64_t q_stride, const int64_t *seq_offsets,

@@ -149,3 +149,10 @@ def test_python_refuses_host_tensors():
         ops.HstuCache.empty(2, 1, 64, "cpu")
     with pytest.raises(ValueError, match="pages of 32"):
         ops.HstuCache(torch.zeros(1, 1, 32, 64), *([None] * 6))
+
+
+def test_a_cache_keeps_its_tensors():
+    cache = object.__new__(ops.HstuCache)
+    cache._structs = {}
+    with pytest.raises(AttributeError, match="keeps its tensors"):
+        cache.weights = None

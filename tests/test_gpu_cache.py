@@ -320,6 +320,81 @@ def test_attention_drops_and_flags(new, cuda_device):
     _check_attn(x, out, want, terms)
 
 
+@pytest.mark.parametrize("new", [3, 66])
+def test_attention_of_more_sequences_than_threads(new, cuda_device):
+    """A thousand sequences, some without a cache, some without new tokens: several units a CTA."""
+    rng = np.random.default_rng(3)
+    n = [int(a) for a in rng.integers(0, 3, 1000) * new // 2]
+    x = _attn_inputs(([int(a) for a in rng.integers(0, 70, 1000)], n, None), "bf16", 64, 1, 47)
+    out, wout, ws, _ = _run_attn(x, cuda_device)
+    assert ops.hstu_check_device_flag(ws) == (0, 0)
+    want, want_w, terms = _want_attn(x)
+    _check_attn(x, out, want, terms, wout, want_w, np.full(want_w.shape, -5.0))
+
+
+@pytest.mark.parametrize("cached,new", [(5000, 300), (900, 129), (130, 500)])
+@pytest.mark.parametrize("same_stamp", [True, False])
+def test_attention_of_candidates(cached, new, same_stamp, cuda_device):
+    """Ranking: all rows candidates, of one stamp (one bias a key) or of several, with a
+    ragged last tile; rows of very different sizes in one of the sequences."""
+    x = _attn_inputs(([cached, 0, cached // 2 + 1], [new, new - 1, new], [new, new - 1, new]), "bf16", 128, 2, 53)
+    if same_stamp:
+        x["ts"][:] = 1_700_000_000 + 10 ** 6
+        x["q"][:new] = _bf16(np.random.default_rng(1).standard_normal((new, 2, 128)))
+    out, wout, ws, _ = _run_attn(x, cuda_device)
+    assert ops.hstu_check_device_flag(ws) == (0, 0)
+    want, want_w, terms = _want_attn(x)
+    _check_attn(x, out, want, terms, wout, want_w, np.full(want_w.shape, -5.0))
+
+
+@pytest.mark.parametrize("new,max_cache", [(0, 100), (1, 0), (200, 0), (200, 100)])
+def test_attention_of_nothing(new, max_cache, cuda_device):
+    """No new tokens (weights are passed on), an empty cache (the addend or zeros)."""
+    lens = [min(100, max_cache), 0]
+    x = _attn_inputs((lens, [new, new], None), "bf16", 64, 2, 59)
+    x["max_len"], x["max_new"] = max_cache, max(new, 1)
+    if max_cache == 0:
+        x["table"] = np.zeros((2, 1), np.int32)
+    for add in (True, False):
+        out, wout, ws, _ = _run_attn(x, cuda_device, add=add)
+        assert ops.hstu_check_device_flag(ws) == (0, 0)
+        want, want_w, terms = _want_attn(x, add=add)
+        _check_attn(x, out, want, terms, wout, want_w, np.full(want_w.shape, -5.0))
+
+
+def test_attention_of_a_page_twice(cuda_device):
+    """Sequences may read the same pages where no weights are taken."""
+    for new in (1, 100):
+        x = _attn_inputs(([200, 200], [new, new], None), "bf16", 64, 2, 61)
+        x["table"][1] = x["table"][0]
+        out, _, ws, _ = _run_attn(x, cuda_device, weights="off")
+        assert ops.hstu_check_device_flag(ws) == (0, 0)
+        want, _, terms = _want_attn(x)
+        _check_attn(x, out, want, terms)
+
+
+def test_calls_on_two_streams_at_once(cuda_device):
+    """Two attentions with a workspace each, in flight together, and one workspace reused
+    for calls of other kinds in turn."""
+    xs = [_attn_inputs(([1500, 700], [n, n], None), "bf16", 128, 2, 67 + n) for n in (150, 4)]
+    alone = [_run_attn(x, cuda_device)[0] for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    outs = []
+    for _ in range(5):
+        for x, st in zip(xs, streams):
+            with torch.cuda.stream(st):
+                outs.append(_run_attn(x, cuda_device)[0])
+    torch.cuda.synchronize()
+    for i, out in enumerate(outs):
+        assert torch.equal(out, alone[i % 2])
+    ws = ops.alloc_workspace(1 << 26, cuda_device)
+    ws.fill_(255)
+    for _ in range(2):
+        for x, want in zip(xs, alone):
+            assert torch.equal(_run_attn(x, cuda_device, ws=ws)[0], want)
+
+
 def test_attention_repeats_itself(cuda_device):
     """The same bytes whatever ran before, on another stream and from a captured graph."""
     for new in (1, 9, 200):
