@@ -381,28 +381,34 @@ cache_move_kernel(const CacheCall c, int keep, int blocks, const int32_t *__rest
     }
     large = __syncthreads_or(large);
     uint8_t *kc = c.k_codes + block_offset<D>(to, c.H, h);
+    if (!large) {
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const int x = tid + i * D, u = x / PK;
-        if (u >= count)
-            continue;
-        uint32_t w[4] = {kw[i].x, kw[i].y, kw[i].z, kw[i].w};
-        const float r = code_ratio(tok_ks[u], ki);
-        const __half2 rh = __half2half2(tok_rk[u]);
+        for (int i = 0; i < 4; i++) {
+            const int x = tid + i * D, u = x / PK;
+            const __half2 r = __half2half2(tok_rk[u]);
+            if (u < count)
+                *reinterpret_cast<uint4 *>(kc + u * D + x % PK * 16) = make_uint4(
+                    put4h(kw[i].x, r, r), put4h(kw[i].y, r, r), put4h(kw[i].z, r, r), put4h(kw[i].w, r, r));
+        }
 #pragma unroll
-        for (int e = 0; e < 4; e++)
-            w[e] = large ? put4(w[e], r, r, r, r) : put4h(w[e], rh, rh);
-        *reinterpret_cast<uint4 *>(kc + u * D + x % PK * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-    }
+        for (int i = 0; i < 16; i++) {
+            const uint2 r = *reinterpret_cast<const uint2 *>(&tok_rv[4 * i]);
+            drow[i] = put4h(drow[i], *reinterpret_cast<const __half2 *>(&r.x), *reinterpret_cast<const __half2 *>(&r.y));
+        }
+    } else {
 #pragma unroll
-    for (int i = 0; i < 16; i++) {
-        const int u = 4 * i;
-        if (large) {
-            const float4 r = *reinterpret_cast<const float4 *>(&tok_vs[u]);
+        for (int i = 0; i < 4; i++) {
+            const int x = tid + i * D, u = x / PK;
+            const float r = code_ratio(tok_ks[u], ki);
+            if (u < count)
+                *reinterpret_cast<uint4 *>(kc + u * D + x % PK * 16) =
+                    make_uint4(put4(kw[i].x, r, r, r, r), put4(kw[i].y, r, r, r, r), put4(kw[i].z, r, r, r, r),
+                               put4(kw[i].w, r, r, r, r));
+        }
+#pragma unroll 1
+        for (int i = 0; i < 16; i++) {
+            const float4 r = *reinterpret_cast<const float4 *>(&tok_vs[4 * i]);
             drow[i] = put4(drow[i], code_ratio(r.x, vi), code_ratio(r.y, vi), code_ratio(r.z, vi), code_ratio(r.w, vi));
-        } else {
-            const __half2 *r = reinterpret_cast<const __half2 *>(&tok_rv[u]);
-            drow[i] = put4h(drow[i], r[0], r[1]);
         }
     }
     __syncwarp();
