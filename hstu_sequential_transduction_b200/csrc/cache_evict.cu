@@ -205,11 +205,22 @@ cache_select_kernel(const CacheCall c, int keep, int first, int recent, const in
     }
 }
 
-// largest magnitude of four codes, as a code
-__device__ __forceinline__ uint32_t max_code(uint32_t w)
+__device__ __forceinline__ __half2 codes_half2(uint32_t codes)
 {
-    const uint32_t m = w & 0x7f7f7f7fu, n = __vmaxu4(m, m >> 16);
-    return max(n & 255u, n >> 8 & 255u);
+    const uint32_t h = e4m3x2_to_f16x2(codes);
+    return *reinterpret_cast<const __half2 *>(&h);
+}
+
+// the larger of m and four codes' magnitudes, two and two
+__device__ __forceinline__ __half2 max_codes(__half2 m, uint32_t w)
+{
+    return __hmax2(m, __hmax2(__habs2(codes_half2(w)), __habs2(codes_half2(w >> 16))));
+}
+
+// bits of the larger of a pair of magnitudes, times the scale
+__device__ __forceinline__ uint32_t magnitude(__half2 m, float scale)
+{
+    return __float_as_uint(fmaxf(__low2float(m), __high2float(m)) * scale) & 0x7fffffffu;
 }
 
 // four codes re-rounded, each with its own ratio: one rounding, the products are exact
@@ -223,9 +234,7 @@ __device__ __forceinline__ uint32_t put4(uint32_t w, float r0, float r1, float r
 // two is exact down to f16's last place, 2^-24, far below E4M3's first tie at 2^-10
 __device__ __forceinline__ uint32_t put4h(uint32_t w, __half2 r01, __half2 r23)
 {
-    const uint32_t a = e4m3x2_to_f16x2(w), b = e4m3x2_to_f16x2(w >> 16);
-    const __half2 x = __hmul2(*reinterpret_cast<const __half2 *>(&a), r01);
-    const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&b), r23);
+    const __half2 x = __hmul2(codes_half2(w), r01), y = __hmul2(codes_half2(w >> 16), r23);
     unsigned short lo, hi;
     asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(lo) : "r"(*reinterpret_cast<const uint32_t *>(&x)));
     asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(hi) : "r"(*reinterpret_cast<const uint32_t *>(&y)));
@@ -312,9 +321,6 @@ cache_move_kernel(const CacheCall c, int keep, int blocks, const int32_t *__rest
     const uint8_t *sbytes = reinterpret_cast<const uint8_t *>(srow);
     uint8_t *dbytes = reinterpret_cast<uint8_t *>(drow);
     uint32_t mk = 0, mv = 0;
-    auto magnitude = [](uint32_t code, float scale) {
-        return __float_as_uint(e4m3x2_to_f32x2(code).x * scale) & 0x7fffffffu;
-    };
 #pragma unroll
     for (int i = 0; i < 16; i++)
         drow[i] = 0u;
@@ -331,27 +337,29 @@ cache_move_kernel(const CacheCall c, int keep, int blocks, const int32_t *__rest
         __syncwarp();
         if (end < count)
             fetch(end);
-        uint32_t top = 0;
+        __half2 top = __half2half2(__ushort_as_half(0));
         const float vs = tok_vs[u];
         while (u < end) {
             if ((u & 3) == 0 && u + 4 <= end) {
                 const int4 sl = *reinterpret_cast<const int4 *>(&tok_slot[u]);
-                const uint32_t x = (uint32_t)sbytes[sl.x] | (uint32_t)sbytes[sl.y] << 8 | (uint32_t)sbytes[sl.z] << 16 |
-                                   (uint32_t)sbytes[sl.w] << 24;
+                const uint32_t lo = __byte_perm(sbytes[sl.x], sbytes[sl.y], 0x0040);
+                const uint32_t hi = __byte_perm(sbytes[sl.z], sbytes[sl.w], 0x0040);
+                const uint32_t x = __byte_perm(lo, hi, 0x5410);
                 drow[u >> 2] = x;
-                top = max(top, max_code(x));
+                top = max_codes(top, x);
                 u += 4;
             } else {
                 const uint32_t x = sbytes[tok_slot[u]];
                 dbytes[u++] = (uint8_t)x;
-                top = max(top, x & 127u);
+                top = max_codes(top, x);
             }
         }
         mv = max(mv, magnitude(top, vs));
     }
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-        const uint32_t top = max(max(max_code(kw[i].x), max_code(kw[i].y)), max(max_code(kw[i].z), max_code(kw[i].w)));
+        __half2 top = __half2half2(__ushort_as_half(0));
+        top = max_codes(max_codes(max_codes(max_codes(top, kw[i].x), kw[i].y), kw[i].z), kw[i].w);
         mk = max(mk, magnitude(top, tok_ks[(tid + i * D) / PK]));
     }
     mk = __reduce_max_sync(0xffffffffu, mk);
