@@ -74,11 +74,11 @@ __device__ __forceinline__ uint32_t word(const uint4 &w, int i) { return i == 0 
 
 // RT: row tiles of 8 (1 or 2)
 template <int D, int RT>
-__global__ void __launch_bounds__(kWarps * 32, RT == 1 ? 3 : 2)
+__global__ void __launch_bounds__(kWarps * 32, RT == 1 || D == 64 ? 3 : 2)
 cache_attn_rows_kernel(const CacheAttnArgs a)
 {
     constexpr int R = 8 * RT, NC = D / 64, VN = D / 16, kBiasLd = R + 2;
-    constexpr int kBlock = kPage * D;
+    constexpr int kBlock = kPage * D, kBiasRows = 8;
     extern __shared__ __align__(16) unsigned char smem[];  // blocks of keys and values per warp, biases
     __shared__ int row_pi[R];
     __shared__ int64_t row_ti[R];
@@ -212,21 +212,24 @@ cache_attn_rows_kernel(const CacheAttnArgs a)
                     rp[pos_index(row_pi[0], pj[e], a.pos_lo, a.pos_hi)] + rt_[time_bucket(row_ti[0], tj[e], a.nb)];
         } else {
 #pragma unroll 1
-            for (int r = 0; r < rows; r += 4) {  // rows behind the last repeat it
-                float bp[8], bt[8];
+            for (int r = 0; r < rows; r += kBiasRows) {  // rows behind the last repeat it
+                float bp[2 * kBiasRows], bt[2 * kBiasRows];
 #pragma unroll
-                for (int x = 0; x < 8; x++) {
+                for (int x = 0; x < 2 * kBiasRows; x++) {
                     bp[x] = rp[pos_index(row_pi[r + (x >> 1)], pj[x & 1], a.pos_lo, a.pos_hi)];
                     bt[x] = rt_[time_bucket(row_ti[r + (x >> 1)], tj[x & 1], a.nb)];
                 }
 #pragma unroll
-                for (int x = 0; x < 8; x++)
+                for (int x = 0; x < 2 * kBiasRows; x++)
                     bias[(lane + 32 * (x & 1)) * kBiasLd + r + (x >> 1)] = bp[x] + bt[x];
             }
         }
         __syncwarp();
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(kbar, loads & 1, &abort_flag, c.hdr))))
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(kbar, loads & 1, &abort_flag, c.hdr)))) {
+            mbar_drain(kbar, loads & 1);
+            mbar_drain(vbar, loads & 1);
             break;
+        }
         float sc[RT][4][4];  // keys of tile m: 16 (g / 2) + 4 m + g % 2 (+ 2), queries 2 t, + 1
         const int key0 = 16 * (g >> 1) + (g & 1);
         const unsigned char *krow = kbuf + key0 * D + 16 * t;
@@ -301,8 +304,11 @@ cache_attn_rows_kernel(const CacheAttnArgs a)
                     wplane[p * kPage + key0 + 2 * i] = wsum[i];
             }
         }
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(vbar, loads & 1, &abort_flag, c.hdr))))
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(vbar, loads & 1, &abort_flag, c.hdr)))) {
+            mbar_drain(kbar, (loads + (next >= 0)) & 1);
+            mbar_drain(vbar, loads & 1);
             break;
+        }
         uint32_t keep[4];  // codes behind the last token may be anything
 #pragma unroll
         for (int e = 0; e < 4; e++) {

@@ -60,7 +60,7 @@ enum Bars { K_FULL = 0, K_EMPTY = K_FULL + kKStages, C_FULL = K_EMPTY + kKStages
             S_FULL = C_EMPTY + kVStages, P_FULL = S_FULL + 4, V_FULL = P_FULL + 4,
             V_EMPTY = V_FULL + 2, KEY_FULL = V_EMPTY + 2, KEY_EMPTY = KEY_FULL + kKeySlots,
             Q_FULL = KEY_EMPTY + kKeySlots, Q_EMPTY = Q_FULL + 2, O_FULL = Q_EMPTY + 2, O_FREE = O_FULL + 1,
-            NBARS = O_FREE + 1 };
+            MMA_DONE = O_FREE + 1, NBARS = MMA_DONE + 2 };
 
 // what the epilogue needs to know of a tile's keys: the bias against column 0 and the scale, both halved (scale -1:
 // no token), position and stamp
@@ -405,7 +405,7 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
 
     if (warp == 0) {
         // ---------------- codes ----------------
-        int g = 0;
+        int g = 0, k_loads = 0, v_loads = 0;
         for (Walk w = start; ok && w.left > 0; w.next(c)) {
             const int h = w.head(), pages = (w.s.len + kPage - 1) / kPage, count = w.count();
             int held = -1, held_scale = 0;  // lane: a page of this and the next 15 tiles, its v_scale's bits
@@ -436,6 +436,7 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
                             tma_load_2d(base + LY::K + kst * LY::KT + e * kPage * D, &tk, 0,
                                         (page[e] * c.H + h) * kPage, bar(K_FULL + kst));
                 }
+                k_loads = g + 1;
                 ok = g < kVStages || wait_all(C_EMPTY + vst, g / kVStages - 1);
                 if (!ok)
                     break;
@@ -448,9 +449,14 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
                             tma_load_2d(base + LY::V + vst * LY::KT + e * kPage * D, &tv, 0,
                                         (page[e] * c.H + h) * D, bar(C_FULL + vst));
                 }
+                v_loads = g + 1;
                 __syncwarp();
             }
         }
+        for (int i = max(k_loads - kKStages, 0); i < k_loads; i++)
+            mbar_drain(bar(K_FULL + i % kKStages), i / kKStages & 1);
+        for (int i = max(v_loads - kVStages, 0); i < v_loads; i++)
+            mbar_drain(bar(C_FULL + i % kVStages), i / kVStages & 1);
     } else if (warp == 1) {
         // ---------------- S^T = K Q^T ----------------
         int g = 0, it = 0;
@@ -918,6 +924,12 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
                 mbar_arrive(bar(Q_EMPTY + qs));
             }
         }
+    }
+    if (warp == 1 || warp == 2) {  // MMAs that an aborting CTA left
+        if (elect_one())
+            umma_commit(bar(MMA_DONE + warp - 1));
+        __syncwarp();
+        mbar_drain(bar(MMA_DONE + warp - 1), 0);
     }
     tc_fence_before();
     __syncthreads();

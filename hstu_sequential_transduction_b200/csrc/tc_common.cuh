@@ -85,6 +85,15 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
     }
 }
 
+// Before the end of a kernel: bounded wait for an asynchronous operation of the CTA's
+// own that still writes shared memory or TMEM, whether or not the CTA aborted.
+__device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity, long long limit = 1 << 24)
+{
+    const long long t0 = clock64();
+    while (!mbar_try_wait(bar, parity) && clock64() - t0 < limit) {
+    }
+}
+
 // ---- TMA --------------------------------------------------------------------
 
 __device__ __forceinline__ void tma_prefetch(const CUtensorMap *map)
