@@ -456,7 +456,7 @@ class HstuCache:
         self.k_codes, self.v_codes, self.k_scale, self.v_scale = k_codes, v_codes, k_scale, v_scale
         self.timestamps, self.positions, self.weights = timestamps, positions, weights
         self.num_pages, self.num_heads, self.head_dim = int(pages), int(heads), int(d)
-        self.device = k_codes.device
+        self.device, self.device_index = k_codes.device, k_codes.get_device()
         self._structs = {}
 
     def __setattr__(self, name, value):
@@ -491,25 +491,25 @@ def _same_device(t, name, device):
         raise ValueError(f"{name} is on {t.device}, the cache on {device}")
 
 
-def _on(device, t, name, dtype) -> int:
+def _on(cache, t, name, dtype) -> int:
     """The address of a dense tensor of this type on the cache's device; 0 for None."""
     if t is None:
         return 0
-    if t.dtype is not dtype or t.get_device() != device.index or not t.is_contiguous():
+    if t.dtype is not dtype or t.get_device() != cache.device_index or not t.is_contiguous():
         _dev(t, name, dtype)
-        _same_device(t, name, device)
+        _same_device(t, name, cache.device)
     return t.data_ptr()
 
 
 def _cache_table(cache, t, name, shape=None) -> int:
-    p = _on(cache.device, t, name, torch.int32)
+    p = _on(cache, t, name, torch.int32)
     if t is not None and (t.dim() != 2 if shape is None else t.shape != shape):
         raise ValueError(f"{name} must be [num_seqs, max_pages]")
     return p
 
 
 def _cache_ints(cache, B, t, name) -> int:
-    p = _on(cache.device, t, name, torch.int32)
+    p = _on(cache, t, name, torch.int32)
     if t is not None and t.numel() != B:
         raise ValueError(f"{name} has {t.numel()} entries for {B} sequences")
     return p
@@ -525,22 +525,31 @@ def _cache_rows(cache, name, t):
     st = t.stride()
     if t.numel() and (st[2] != 1 or (H > 1 and st[1] != d)):
         raise ValueError(f"{name} must have dense rows")
-    if t.get_device() != cache.device.index:
+    if t.get_device() != cache.device_index:
         _same_device(t, name, cache.device)
     return st[0] if t.shape[0] > 1 else H * d
 
 
 def _cache_tokens(cache, B, T, seq_offsets, timestamps):
-    off = _on(cache.device, seq_offsets, "seq_offsets", torch.int64)
-    ts = _on(cache.device, timestamps, "timestamps", torch.int64)
+    off = _on(cache, seq_offsets, "seq_offsets", torch.int64)
+    ts = _on(cache, timestamps, "timestamps", torch.int64)
     if seq_offsets.numel() != B + 1 or timestamps.numel() != T:
         raise ValueError(f"seq_offsets needs {B + 1} entries and timestamps {T}")
     return off, ts
 
 
-def _cache_workspace(cache, workspace, need):
+def _cache_empty(cache, stream, shape, dtype):
+    """A new tensor on the stream of the call: the allocator gives its memory out again by that stream's order."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=cache.device)
+    with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else
+                           torch.cuda.ExternalStream(_cache_stream(cache, stream), device=cache.device)):
+        return torch.empty(shape, dtype=dtype, device=cache.device)
+
+
+def _cache_workspace(cache, stream, workspace, need):
     if workspace is None:
-        return alloc_workspace(need, cache.device)
+        return _cache_empty(cache, stream, max(need, 256), torch.uint8)
     _same_device(workspace, "workspace", cache.device)
     return workspace
 
@@ -548,7 +557,7 @@ def _cache_workspace(cache, workspace, need):
 def _cache_call(cache, name, stream, *args):
     """Calls into the library on the cache's device and, by default, that device's current stream."""
     fn = getattr(load_library(), name)
-    if torch.cuda.current_device() == cache.device.index:
+    if torch._C._cuda_getDevice() == cache.device_index:
         status = fn(*args, _cache_stream(cache, stream))
     else:
         with torch.cuda.device(cache.device):
@@ -558,8 +567,12 @@ def _cache_call(cache, name, stream, *args):
 
 def _cache_stream(cache, stream):
     if stream is None:  # the raw handle: a Stream object costs 2 us
-        return torch._C._cuda_getCurrentRawStream(cache.device.index)
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        return torch._C._cuda_getCurrentRawStream(cache.device_index)
+    if not hasattr(stream, "cuda_stream"):
+        return int(stream)
+    if stream.device != cache.device:
+        raise ValueError(f"the stream is on {stream.device}, the cache on {cache.device}")
+    return stream.cuda_stream
 
 
 def hstu_cache_append_workspace_size() -> int:
@@ -584,10 +597,10 @@ def hstu_cache_append(k, v, cache: HstuCache, block_table, cache_lens, seq_pos, 
     T = k.shape[0]
     off, ts = _cache_tokens(cache, B, T, seq_offsets, timestamps)
     if new_lens is None:
-        new_lens = torch.empty_like(cache_lens)
+        new_lens = _cache_empty(cache, stream, B, torch.int32)
     if new_pos is None:
-        new_pos = torch.empty_like(cache_lens)
-    workspace = _cache_workspace(cache, workspace, 256)
+        new_pos = _cache_empty(cache, stream, B, torch.int32)
+    workspace = _cache_workspace(cache, stream, workspace, 256)
     _cache_call(cache, "hstu_cache_append", stream, cache.struct(cols), _dtype_code(k), B, int(max_seq_len), T, k.data_ptr(), sk,
                 v.data_ptr(), sv, off, ts, nt, table, lens, pos, _cache_ints(cache, B, new_lens, "new_lens"),
                 _cache_ints(cache, B, new_pos, "new_pos"), workspace.data_ptr(), workspace.numel())
@@ -626,10 +639,10 @@ def hstu_cache_attn_fwd(q, cache: HstuCache, block_table, cache_lens, seq_pos, s
     nt = _cache_ints(cache, B, num_targets, "num_targets")
     sq = _cache_rows(cache, "q", q)
     off, ts = _cache_tokens(cache, B, q.shape[0], seq_offsets, timestamps)
-    rp = _on(cache.device, rab_pos, "rab_pos", torch.float32)
-    rt = _on(cache.device, rab_time, "rab_time", torch.float32)
+    rp = _on(cache, rab_pos, "rab_pos", torch.float32)
+    rt = _on(cache, rab_time, "rab_time", torch.float32)
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=cache.device)
+        out = _cache_empty(cache, stream, q.shape, q.dtype)
     for name, t in (("addend", addend), ("out", out)):
         if t is not None and t.shape != q.shape:
             raise ValueError(f"{name} must have q's shape")
@@ -638,16 +651,17 @@ def hstu_cache_attn_fwd(q, cache: HstuCache, block_table, cache_lens, seq_pos, s
     desc = ctypes.byref(_cache_attn_desc(q, block_table, rab_pos, rab_time, max_seq_len, inv_n, pos_lo, pos_hi,
                                          cand_own_index))
     pool = cache.struct(cols)
+    need = 0
     if workspace is None:
         n = ctypes.c_size_t(0)
         with torch.cuda.device(cache.device):
             _check("hstu_cache_attn_workspace_size", load_library().hstu_cache_attn_workspace_size(
                 desc, pool, int(max_cache_len), int(weights_out is not None), ctypes.byref(n)))
-        workspace = alloc_workspace(n.value, cache.device)
-    _same_device(workspace, "workspace", cache.device)
+        need = n.value
+    workspace = _cache_workspace(cache, stream, workspace, need)
     _cache_call(cache, "hstu_cache_attn_fwd", stream, desc, pool, int(max_cache_len), q.data_ptr(), sq, off, ts, nt, rp, rt,
-                table, lens, pos, _on(cache.device, addend, "addend", q.dtype),
-                _on(cache.device, weights_out, "weights_out", torch.float32), _on(cache.device, out, "out", q.dtype),
+                table, lens, pos, _on(cache, addend, "addend", q.dtype),
+                _on(cache, weights_out, "weights_out", torch.float32), _on(cache, out, "out", q.dtype),
                 workspace.data_ptr(), workspace.numel())
     return out
 
@@ -672,22 +686,21 @@ def hstu_cache_evict(cache: HstuCache, block_table, cache_lens, new_pages, *, ke
     if cache.weights is None:
         raise ValueError("eviction needs the cache's weights")
     if new_table is None:
-        new_table = torch.empty_like(block_table)
+        new_table = _cache_empty(cache, stream, (B, cols), torch.int32)
     if new_lens is None:
-        new_lens = torch.empty_like(cache_lens)
+        new_lens = _cache_empty(cache, stream, B, torch.int32)
     if kept is None:
-        kept = torch.empty((B, keep), dtype=torch.int32, device=cache.device)
+        kept = _cache_empty(cache, stream, (B, keep), torch.int32)
     if tuple(kept.shape) != (B, keep):
         raise ValueError(f"kept must be [{B}, {keep}]")
-    if workspace is None:
-        workspace = alloc_workspace(hstu_cache_evict_workspace_size(cache, block_table, keep=keep,
-                                                                    max_cache_len=max_cache_len), cache.device)
-    _same_device(workspace, "workspace", cache.device)
+    need = 0 if workspace is not None else hstu_cache_evict_workspace_size(cache, block_table, keep=keep,
+                                                                           max_cache_len=max_cache_len)
+    workspace = _cache_workspace(cache, stream, workspace, need)
     _cache_call(cache, "hstu_cache_evict", stream, cache.struct(cols), B, int(max_cache_len), keep, int(first), int(recent), table,
                 _cache_ints(cache, B, cache_lens, "cache_lens"),
                 _cache_table(cache, new_pages, "new_pages", block_table.shape),
                 _cache_table(cache, new_table, "new_table", block_table.shape),
-                _cache_ints(cache, B, new_lens, "new_lens"), _on(cache.device, kept, "kept", torch.int32),
+                _cache_ints(cache, B, new_lens, "new_lens"), _on(cache, kept, "kept", torch.int32),
                 workspace.data_ptr(), workspace.numel())
     return new_table, new_lens, kept
 

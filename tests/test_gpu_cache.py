@@ -637,3 +637,38 @@ def test_captured_serving_step(cuda_device):
         assert torch.equal(eager["out"], replay["out"])
     assert eager["lens"].tolist() == [steps] * B
     assert_pool_equal(pool_of(replay["cache"]), pool_of(eager["cache"]))
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_what_a_call_allocates_belongs_to_its_stream(raw, cuda_device, monkeypatch):
+    """Memory of another stream's could be given out again while the call still runs."""
+    made = []
+
+    def recorded(*args, real=ops._cache_empty):
+        made.append(real(*args))
+        return made[-1]
+
+    monkeypatch.setattr(ops, "_cache_empty", recorded)
+    side = torch.cuda.Stream()
+    stream = side.cuda_stream if raw else side
+    x = _attn_inputs(([300, 70], [3, 3], None), "bf16", 64, 2, 91)
+    cache = to_cache(x["pool"], cuda_device, weights=True)
+    g = {n: dev(x[n], cuda_device) for n in ("table", "lens", "seq_pos", "off", "ts", "rp", "rt")}
+    q = x["q"].to(cuda_device)
+    new_pages = np.full(x["table"].shape, -1, np.int32)
+    new_pages[:, 0] = np.setdiff1d(np.arange(len(x["pool"]["positions"])), x["table"])[:2]
+    new_pages = dev(new_pages, cuda_device)
+    args = dict(max_seq_len=3, max_cache_len=300, inv_n=1 / 64, pos_lo=-100, pos_hi=100)
+    torch.cuda.synchronize()
+    out = ops.hstu_cache_attn_fwd(q, cache, g["table"], g["lens"], g["seq_pos"], g["off"], g["ts"], None, g["rp"],
+                                  g["rt"], stream=stream, **args)
+    ops.hstu_cache_append(q, q, cache, g["table"], g["lens"], g["seq_pos"], g["off"], g["ts"], None, max_seq_len=3,
+                          stream=stream)
+    ops.hstu_cache_evict(cache, g["table"], g["lens"], new_pages, keep=64, max_cache_len=300, stream=stream)
+    torch.cuda.synchronize()
+    owners = [[seg["stream"] for seg in torch.cuda.memory_snapshot()
+               if seg["address"] <= t.data_ptr() < seg["address"] + seg["total_size"]] for t in made]
+    assert len(made) == 9 and owners == [[side.cuda_stream]] * 9
+    want = ops.hstu_cache_attn_fwd(q, to_cache(x["pool"], cuda_device), g["table"], g["lens"], g["seq_pos"], g["off"],
+                                   g["ts"], None, g["rp"], g["rt"], **args)
+    assert torch.equal(out, want)
