@@ -3,9 +3,11 @@
 // Select (one CTA per sequence): weights become integers that compare as the weights
 // do (NaN 0), the first 16 a thread in registers.  Histograms in shared memory of 11, 11
 // and 10 bits find the m-th largest of the unprotected tokens; the first digit holds two
-// bits of the fraction, for weights share few exponents and would crowd into few bins
-// (8-bit digits: 30 us for 12,288 tokens; a count per bit: 33 us).  Ballots and two scans
-// then place the kept indices, ties to the lowest.
+// bits of the fraction, for weights share few exponents and would crowd into few bins.
+// Two scans then place the kept indices, ties to the lowest.  Bound by one SM's
+// instructions: a thread takes four neighbours at a time, which share a page lookup and
+// count as one byte of a packed scan (14 us for 32 sequences of 12,288 tokens; 25 with
+// a lookup and a ballot per token, 33 with a count per bit of the key).
 //
 // Move (one CTA per new block and head, a thread per dim): keys are gathered as rows of
 // 16-byte pieces.  Values are stored transposed: a thread takes its dim's row of every
@@ -31,31 +33,60 @@ __device__ __forceinline__ uint32_t weight_key(float w)
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-constexpr int kSelKeys = 16;  // keys a thread keeps in registers
+constexpr int kSelGroups = 4;  // of four neighbours each: the keys a thread keeps in registers
 
-// In place, exclusive prefix sums of counts[0, 16 kWarps); returns the total.
-template <int kWarps>
-__device__ __forceinline__ int scan_counts(int *counts, int *slots)
+// In place, exclusive prefix sums of counts[0, N); returns the total.
+template <int N>
+__device__ __forceinline__ int scan_counts(int *counts, int *total)
 {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     __syncthreads();
-    int x = tid < kSelKeys * kWarps ? counts[tid] : 0, inc = x;
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        int x[N / 32], sum = 0;
+#pragma unroll
+        for (int e = 0; e < N / 32; e++)
+            sum += x[e] = counts[lane * (N / 32) + e];
+        int inc = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o)
+                inc += y;
+        }
+        if (lane == 31)
+            *total = inc;
+        int before = inc - sum;
+#pragma unroll
+        for (int e = 0; e < N / 32; e++) {
+            counts[lane * (N / 32) + e] = before;
+            before += x[e];
+        }
+    }
+    __syncthreads();
+    return *total;
+}
+
+// How many of the bits of each group (a nibble of `bits`) the lanes below hold, a byte a
+// group (a warp holds 128 at most); the warp's counts go to counts[group * warps + warp].
+__device__ __forceinline__ uint32_t rank_groups(uint32_t bits, int *counts, int warps)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint32_t mine = 0;
+#pragma unroll
+    for (int i = 0; i < kSelGroups; i++)
+        mine |= __popc(bits >> (4 * i) & 15u) << (8 * i);
+    uint32_t inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, inc, o);
+        const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o)
             inc += y;
     }
     if (lane == 31)
-        slots[warp] = inc;
-    __syncthreads();
-    const int mine = lane < kWarps ? slots[lane] : 0;
-    const int before = __reduce_add_sync(0xffffffffu, lane < warp ? mine : 0);
-    const int total = __reduce_add_sync(0xffffffffu, mine);
-    if (tid < kSelKeys * kWarps)
-        counts[tid] = before + inc - x;
-    __syncthreads();
-    return total;
+#pragma unroll
+        for (int i = 0; i < kSelGroups; i++)
+            counts[i * warps + warp] = inc >> (8 * i) & 255u;
+    return inc - mine;
 }
 
 template <int kSelThreads>
@@ -65,7 +96,7 @@ cache_select_kernel(const CacheCall c, int keep, int first, int recent, const in
                     uint32_t *__restrict__ keys, int64_t cap)
 {
     constexpr int kSelWarps = kSelThreads / 32, kBins = 2048;
-    __shared__ int slots[2][32], counts[kSelKeys * kSelWarps], bins[kBins], found[3];
+    __shared__ int slots[2][32], counts[kSelGroups * kSelWarps], bins[kBins], found[3], total;
     const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const CacheSeq s = cache_seq(c, b);
     const int L = s.len;
@@ -86,21 +117,40 @@ cache_select_kernel(const CacheCall c, int keep, int first, int recent, const in
     }
     const int late = min(keep, recent), early = min(min(keep - late, first), L - late);
     const int m = keep - late - early;  // of the tokens [early, L - late)
-    constexpr int kRound = kSelKeys * kSelThreads;
+    constexpr int kStep = 4 * kSelThreads, kRound = kSelGroups * kStep;
     uint32_t *rest = keys + (int64_t)b * cap;  // the keys from kRound on
+    const int32_t *table = c.table + (int64_t)b * c.max_pages;
     bool bad = false;
-    auto open = [&](int j) { return j >= early && j < L - late; };
-    auto key_of = [&](int j) {  // 0 for a protected token too
-        const int page = table_page(c.table, c, b, j / kPage);
-        bad |= page < 0;
-        return page < 0 || !open(j) ? 0u : weight_key(c.weights[(int64_t)page * kPage + j % kPage]);
-    };
-    uint32_t key[kSelKeys];  // of tokens tid + 1024 i
+    auto open = [&](int j) { return (unsigned)(j - early) < (unsigned)(L - late - early); };
+    // of the four tokens from j on: which are open, and their keys (on a page that is none: 0)
+    auto load4 = [&](int j, int entry, uint32_t *key) {
+        const bool known = entry >= 0 && entry < c.num_pages;
+        bad |= !known && j < L;
+        const float *w = c.weights + (int64_t)(known ? entry : 0) * kPage + j % kPage;
+        uint32_t bits = 0;
 #pragma unroll
-    for (int i = 0; i < kSelKeys; i++)
-        key[i] = i * kSelThreads + tid < L ? key_of(i * kSelThreads + tid) : 0u;
-    for (int j = kRound + tid; j < L; j += kSelThreads)  // read again by this thread only
-        rest[j] = key_of(j);
+        for (int e = 0; e < 4; e++) {
+            const float x = w[e];
+            key[e] = known ? weight_key(x) : 0u;
+            bits |= (uint32_t)open(j + e) << e;
+        }
+        return bits;
+    };
+    // the thread's tokens are 4 tid + kStep i + (0 .. 3)
+    uint32_t key[4 * kSelGroups], opens = 0;
+    int entry[kSelGroups];
+#pragma unroll
+    for (int i = 0; i < kSelGroups; i++)
+        entry[i] = table[min(4 * tid + kStep * i, L - 1) / kPage];
+#pragma unroll
+    for (int i = 0; i < kSelGroups; i++)
+        opens |= load4(4 * tid + kStep * i, entry[i], key + 4 * i) << (4 * i);
+    for (int j = kRound + 4 * tid; j < L; j += kStep) {  // read again by this thread only
+        uint32_t k4[4];
+        load4(j, table[j / kPage], k4);
+        for (int e = 0; e < min(L - j, 4); e++)
+            rest[j + e] = k4[e];
+    }
     if (bad)
         atomicOr(&c.hdr->flag, FLAG_CACHE_PAGE);
     // prefix: the m-th largest open key, of whose equals the first `ties` are kept; with
@@ -113,12 +163,13 @@ cache_select_kernel(const CacheCall c, int keep, int first, int recent, const in
             bins[i] = 0;
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < kSelKeys; i++)
-            if (open(i * kSelThreads + tid) && (key[i] & mask) == prefix)
+        for (int i = 0; i < 4 * kSelGroups; i++)
+            if ((opens >> i & 1) && (key[i] & mask) == prefix)
                 atomicAdd(&bins[key[i] >> shift & (n - 1)], 1);
-        for (int j = kRound + tid; j < L; j += kSelThreads)
-            if (open(j) && (rest[j] & mask) == prefix)
-                atomicAdd(&bins[rest[j] >> shift & (n - 1)], 1);
+        for (int j = kRound + 4 * tid; j < L; j += kStep)
+            for (int e = 0; e < min(L - j, 4); e++)
+                if (open(j + e) && (rest[j + e] & mask) == prefix)
+                    atomicAdd(&bins[rest[j + e] >> shift & (n - 1)], 1);
         __syncthreads();
         // from the highest bin down, the one in which the running count reaches `ties`
         const int per = n / kSelThreads, top = n - 1 - tid * per;
@@ -157,51 +208,58 @@ cache_select_kernel(const CacheCall c, int keep, int first, int recent, const in
         n = shift == 21 ? kBins : 1024;  // digits at 21, 10 and 0
         __syncthreads();
     }
-    // in rounds of 16 x 1024 tokens: what each warp's 32 tokens hold, scanned
-    const uint32_t below = (1u << lane) - 1u;
+    // in rounds of kRound tokens, in order of group, warp, lane
     int ties_before = 0, out_before = 0;
     for (int j0 = 0; j0 < L; j0 += kRound) {
-        if (j0 > 0)
+        if (j0 > 0) {
+            opens = 0;
 #pragma unroll
-            for (int i = 0; i < kSelKeys; i++)
-                key[i] = j0 + i * kSelThreads + tid < L ? rest[j0 + i * kSelThreads + tid] : 0u;
-        uint32_t safe = 0, tie = 0;  // bit i: token i of this thread
-#pragma unroll
-        for (int i = 0; i < kSelKeys; i++) {
-            const int j = j0 + i * kSelThreads + tid;
-            const bool is_tie = m > 0 && !exact && open(j) && key[i] == prefix;
-            const bool is_safe = j < L && (!open(j) || (m > 0 && (exact ? (key[i] & mask) >= prefix : key[i] > prefix)));
-            safe |= (uint32_t)is_safe << i;
-            tie |= (uint32_t)is_tie << i;
-            const uint32_t votes = __ballot_sync(0xffffffffu, is_tie);
-            if (lane == 0)
-                counts[i * kSelWarps + warp] = __popc(votes);
+            for (int i = 0; i < 4 * kSelGroups; i++) {
+                const int j = j0 + 4 * tid + kStep * (i / 4) + i % 4;
+                key[i] = j < L ? rest[j] : 0u;
+                opens |= (uint32_t)open(j) << i;
+            }
         }
-        const int n_ties = scan_counts<kSelWarps>(counts, slots[turn ^= 1]);
-        uint32_t take = safe;
+        uint32_t take = 0, tie = 0;  // bit i: the thread's token i
 #pragma unroll
-        for (int i = 0; i < kSelKeys; i++) {
-            const uint32_t votes = __ballot_sync(0xffffffffu, tie >> i & 1);
-            const int rank = ties_before + counts[i * kSelWarps + warp] + __popc(votes & below);
-            take |= (uint32_t)((tie >> i & 1) && rank < ties) << i;
+        for (int i = 0; i < 4 * kSelGroups; i++) {
+            take |= (uint32_t)(exact ? (key[i] & mask) >= prefix : key[i] > prefix) << i;
+            tie |= (uint32_t)(key[i] == prefix) << i;
         }
-        __syncthreads();
+        uint32_t live = 0;
 #pragma unroll
-        for (int i = 0; i < kSelKeys; i++) {
-            const uint32_t votes = __ballot_sync(0xffffffffu, take >> i & 1);
-            if (lane == 0)
-                counts[i * kSelWarps + warp] = __popc(votes);
+        for (int i = 0; i < kSelGroups; i++) {
+            const int left = L - (j0 + 4 * tid + kStep * i);
+            live |= (left >= 4 ? 15u : left > 0 ? (1u << left) - 1u : 0u) << (4 * i);
         }
-        const int n_out = scan_counts<kSelWarps>(counts, slots[turn ^= 1]);
+        take = ((m > 0 ? take : 0u) | ~opens) & live;
+        if (m > 0 && !exact) {
+            tie &= opens;
+            const uint32_t below = rank_groups(tie, counts, kSelWarps);
+            const int n_ties = scan_counts<kSelGroups * kSelWarps>(counts, &total);
 #pragma unroll
-        for (int i = 0; i < kSelKeys; i++) {
-            const uint32_t votes = __ballot_sync(0xffffffffu, take >> i & 1);
-            if (take >> i & 1)
-                out[out_before + counts[i * kSelWarps + warp] + __popc(votes & below)] = j0 + i * kSelThreads + tid;
+            for (int i = 0; i < kSelGroups; i++) {
+                int rank = ties_before + counts[i * kSelWarps + warp] + (int)(below >> (8 * i) & 255u);
+#pragma unroll
+                for (int e = 4 * i; e < 4 * i + 4; e++)
+                    if (tie >> e & 1)
+                        take |= (uint32_t)(rank++ < ties) << e;
+            }
+            ties_before += n_ties;
+            __syncwarp();
         }
-        __syncthreads();
-        ties_before += n_ties;
+        const uint32_t below = rank_groups(take, counts, kSelWarps);
+        const int n_out = scan_counts<kSelGroups * kSelWarps>(counts, &total);
+#pragma unroll
+        for (int i = 0; i < kSelGroups; i++) {
+            int at = out_before + counts[i * kSelWarps + warp] + (int)(below >> (8 * i) & 255u);
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+                if (take >> (4 * i + e) & 1)
+                    out[at++] = j0 + 4 * tid + kStep * i + e;
+        }
         out_before += n_out;
+        __syncwarp();
     }
 }
 
@@ -456,7 +514,7 @@ cudaError_t launch_cache_evict(const CacheCall &c, int keep, int first, int rece
     if (c.B == 0)
         return cudaSuccess;
     // all keys in the registers of 256 threads, whose barriers are cheap, or of 1024
-    if (c.max_cache_len <= kSelKeys * 256)
+    if (c.max_cache_len <= 4 * kSelGroups * 256)
         cache_select_kernel<256><<<c.B, 256, 0, stream>>>(c, keep, first, recent, new_pages, new_table, new_lens, kept,
                                                           keys, cap);
     else
