@@ -232,13 +232,15 @@ hstu_status attn_bwd_strided(const hstu_attn_desc *desc, const void *q, int64_t 
 
 // ---- 8-bit cache ---------------------------------------------------------------
 
+constexpr int kCacheTokens = INT_MAX - 65535;  // token indices of whole rounds stay within 32 bits
+
 hstu_status check_cache(const hstu_cache *c)
 {
     if (!c || c->num_pages < 1 || c->num_heads < 1 || c->max_pages < 0)
         return HSTU_ERR_INVALID_ARG;
     if (c->head_dim != 32 && c->head_dim != 64 && c->head_dim != 128)
         return HSTU_ERR_UNSUPPORTED;
-    if ((int64_t)c->max_pages * HSTU_CACHE_PAGE > INT_MAX)
+    if ((int64_t)c->max_pages * HSTU_CACHE_PAGE > kCacheTokens)
         return HSTU_ERR_UNSUPPORTED;
     if (!c->k_codes || !c->v_codes || !c->k_scale || !c->v_scale || !c->timestamps || !c->positions ||
         !aligned16(c->k_codes) || !aligned16(c->v_codes))
@@ -904,6 +906,8 @@ hstu_status hstu_cache_evict_workspace_size(const hstu_cache *cache, int32_t num
     HSTU_TRY(check_cache(cache));
     if (num_seqs < 0 || max_cache_len < 0 || keep < 1 || !bytes)
         return HSTU_ERR_INVALID_ARG;
+    if (max_cache_len > kCacheTokens)
+        return HSTU_ERR_UNSUPPORTED;
     *bytes = sizeof(WsHeader) + (max_cache_len > keep ? sizeof(uint32_t) * (size_t)num_seqs * max_cache_len : 0);
     return HSTU_OK;
 }

@@ -326,7 +326,7 @@ typedef struct {
     int32_t num_pages;  /* pages of the pool, >= 1 */
     int32_t num_heads;  /* H */
     int32_t head_dim;   /* d */
-    int32_t max_pages;  /* columns of a block table */
+    int32_t max_pages;  /* columns of a block table, 64 max_pages <= 2^31 - 65536 */
     uint8_t *k_codes, *v_codes;
     float *k_scale, *v_scale;
     int64_t *timestamps;

@@ -130,6 +130,17 @@ def test_evict_refusals(kw, status):
     assert _evict(**kw) == status
 
 
+def test_more_tokens_than_indices_reach():
+    """Kernels round token indices up to whole rounds within 32 bits."""
+    most = 2 ** 31 - 65536
+    for cols, status in ((most // 64, WORKSPACE), (most // 64 + 1, UNSUPPORTED), (2 ** 25 - 1, UNSUPPORTED)):
+        pool = _pool(max_pages=cols)
+        assert _attn(pool=pool, max_cache=64 * min(cols, 2 ** 25 - 1), ws=0) == status
+        assert _evict(pool=pool, ws=0) == status
+    assert _evict(max_cache=most, ws=0) == WORKSPACE
+    assert _evict(max_cache=most + 1, ws=0) == UNSUPPORTED
+
+
 def test_evict_needs_weights():
     assert _evict(pool=_pool(weights=0)) == INVALID
 
