@@ -33,6 +33,18 @@ struct Eight16 {
         const uint32_t x = e < 2 ? w.x : e < 4 ? w.y : e < 6 ? w.z : w.w;
         return __uint_as_float(e & 1 ? x & 0xffff0000u : x << 16);
     }
+    // the larger of m and this one's magnitudes, each parity's: NaN wins
+    using Max = __nv_bfloat162;
+    static __device__ __forceinline__ Max none() { return __nv_bfloat162(__ushort_as_bfloat16(0), __ushort_as_bfloat16(0)); }
+    static __device__ __forceinline__ Max two(Max m, uint32_t x)
+    {
+        return __hmax2_nan(m, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&x)));
+    }
+    __device__ __forceinline__ Max max(Max m) const { return two(two(two(two(m, w.x), w.y), w.z), w.w); }
+    static __device__ __forceinline__ uint32_t bits(Max m)  // as a float's
+    {
+        return (uint32_t)__bfloat16_as_ushort(__hmax_nan(m.x, m.y)) << 16;
+    }
 };
 
 struct Eight32 {
@@ -48,6 +60,16 @@ struct Eight32 {
         const float4 &f = e < 4 ? a : b;
         return (e & 3) == 0 ? f.x : (e & 3) == 1 ? f.y : (e & 3) == 2 ? f.z : f.w;
     }
+    using Max = uint32_t;
+    static __device__ __forceinline__ Max none() { return 0; }
+    __device__ __forceinline__ Max max(Max m) const
+    {
+#pragma unroll
+        for (int e = 0; e < 8; e++)
+            m = ::max(m, __float_as_uint(get(e)) & 0x7fffffffu);
+        return m;
+    }
+    static __device__ __forceinline__ uint32_t bits(Max m) { return m; }
 };
 
 template <typename T> struct EightOf { using type = Eight32; };
@@ -96,8 +118,8 @@ cache_append_kernel(const CacheCall c, const T *__restrict__ k, int64_t ldk, con
     // row of slot t: the sequence's token blk * 64 + t - len
     const int64_t row0 = s.s0 + (int64_t)blk * kPage - s.len;
 
-    typename EightOf<T>::type x[4], y[4];
-    uint32_t mk = 0, mv = 0;
+    using Eight = typename EightOf<T>::type;
+    Eight x[4], y[4];
 #pragma unroll
     for (int t = 0; t < 4; t++) {
         if (t0 + t >= a && t0 + t < end) {
@@ -116,15 +138,13 @@ cache_append_kernel(const CacheCall c, const T *__restrict__ k, int64_t ldk, con
     }
     const int64_t si = (int64_t)page * c.H + h;
     const float kold = a > 0 ? c.k_scale[si] : 0.f, vold = a > 0 ? c.v_scale[si] : 0.f;
+    typename Eight::Max tk = Eight::none(), tv = Eight::none();
 #pragma unroll
-    for (int t = 0; t < 4; t++)
-#pragma unroll
-        for (int e = 0; e < 8; e++) {
-            mk = max(mk, __float_as_uint(x[t].get(e)) & 0x7fffffffu);
-            mv = max(mv, __float_as_uint(y[t].get(e)) & 0x7fffffffu);
-        }
-    mk = __reduce_max_sync(0xffffffffu, mk);
-    mv = __reduce_max_sync(0xffffffffu, mv);
+    for (int t = 0; t < 4; t++) {
+        tk = x[t].max(tk);
+        tv = y[t].max(tv);
+    }
+    uint32_t mk = __reduce_max_sync(0xffffffffu, Eight::bits(tk)), mv = __reduce_max_sync(0xffffffffu, Eight::bits(tv));
     if ((threadIdx.x & 31) == 0) {
         smax[0][threadIdx.x >> 5] = mk;
         smax[1][threadIdx.x >> 5] = mv;
