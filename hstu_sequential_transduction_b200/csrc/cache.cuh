@@ -54,6 +54,13 @@ __device__ __forceinline__ CacheSeq cache_seq(const CacheCall &c, int b)
     return s;
 }
 
+// What is wrong with the offsets as a whole, for the thread that reports sequence b.
+__device__ __forceinline__ int cache_offset_bits(const CacheCall &c, int b)
+{
+    return (b == 0 && c.seq_offsets[0] != 0 ? FLAG_OFFSET0 : 0) |
+           (b == c.B - 1 && c.seq_offsets[c.B] != c.T ? FLAG_TOTAL : 0);
+}
+
 // Page p of sequence b, or -1 where the table names none of the pool.
 __device__ __forceinline__ int table_page(const int32_t *table, const CacheCall &c, int b, int p)
 {

@@ -101,11 +101,7 @@ cache_append_kernel(const CacheCall c, const T *__restrict__ k, int64_t ldk, con
         new_lens[b] = c.cache_lens[b] + count;
         if (new_pos)
             new_pos[b] = s.pos + count;
-        int bits = s.bits;
-        if (b == 0 && c.seq_offsets[0] != 0)
-            bits |= FLAG_OFFSET0;
-        if (b == c.B - 1 && c.seq_offsets[c.B] != c.T)
-            bits |= FLAG_TOTAL;
+        const int bits = s.bits | cache_offset_bits(c, b);
         if (bits)
             atomicOr(&c.hdr->flag, bits);
     }
@@ -242,7 +238,7 @@ cudaError_t launch_cache_append(const CacheCall &c, bool bf16, const void *k, in
                                 int32_t *new_lens, int32_t *new_pos, cudaStream_t stream)
 {
     if (c.B == 0)
-        return cudaSuccess;
+        return launch_cache_no_sequences(c, stream);
     const int blocks = cache_append_blocks(c.max_seq_len);
     if (bf16)
         return c.d == 64 ? append<__nv_bfloat16, 64>(c, k, ldk, v, ldv, new_lens, new_pos, blocks, stream)

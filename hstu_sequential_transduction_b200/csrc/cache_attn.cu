@@ -150,8 +150,11 @@ cache_join_kernel(const CacheAttnArgs a, int row_blocks, int w_blocks)
     if ((int64_t)blockIdx.x < (int64_t)row_blocks * c.B) {
         const int b = blockIdx.x / row_blocks, chunk = blockIdx.x % row_blocks;
         const CacheSeq s = cache_seq(c, b);
-        if (s.bits && chunk == 0 && threadIdx.x == 0)
-            atomicOr(&c.hdr->flag, s.bits);
+        if (chunk == 0 && threadIdx.x == 0) {
+            const int bits = s.bits | cache_offset_bits(c, b);
+            if (bits)
+                atomicOr(&c.hdr->flag, bits);
+        }
         const int nsp = ((s.len + kPage - 1) / kPage + a.plan.split_pages - 1) / a.plan.split_pages;
         const int64_t e = ((int64_t)chunk * 256 + threadIdx.x) * 4;  // four elements of a row
         if (e >= (int64_t)s.n * width)
@@ -175,6 +178,12 @@ cache_join_kernel(const CacheAttnArgs a, int row_blocks, int w_blocks)
     cache_join_weights(a, x / w_blocks, ((x % w_blocks) * 256 + threadIdx.x) * 4);
 }
 
+// A call without sequences: its offsets are one number, and every row is uncovered.
+__global__ void cache_no_sequences_kernel(const int64_t *seq_offsets, int64_t T, WsHeader *hdr)
+{
+    hdr->flag = (seq_offsets[0] != 0 ? FLAG_OFFSET0 : 0) | (seq_offsets[0] != T ? FLAG_TOTAL : 0);
+}
+
 int row_blocks(const CacheCall &c)  // one at least: it reports a sequence that was dropped
 {
     return (int)std::max<int64_t>(1, ((int64_t)c.max_seq_len * c.H * c.d + 1023) / 1024);
@@ -190,6 +199,12 @@ cudaError_t join(const CacheAttnArgs &a, cudaStream_t stream)
 }
 
 }  // namespace
+
+cudaError_t launch_cache_no_sequences(const CacheCall &c, cudaStream_t stream)
+{
+    cache_no_sequences_kernel<<<1, 1, 0, stream>>>(c.seq_offsets, c.T, c.hdr);
+    return cudaGetLastError();
+}
 
 CacheAttnPlan cache_attn_plan(const CacheCall &c, bool bf16, bool with_weights)
 {
@@ -233,7 +248,7 @@ bool cache_attn_fits(const CacheAttnArgs &a)
 cudaError_t launch_cache_attn(const CacheAttnArgs &a, bool bf16, cudaStream_t stream)
 {
     if (a.c.B == 0)
-        return cudaSuccess;
+        return launch_cache_no_sequences(a.c, stream);
     if (a.plan.kernel == CACHE_TC)
         return launch_cache_attn_tc(a, stream);
     const int64_t grid = (int64_t)a.c.B * a.plan.qtiles * a.c.H * a.plan.nsplit;

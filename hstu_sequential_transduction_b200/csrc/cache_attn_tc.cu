@@ -976,8 +976,11 @@ cache_tc_join_kernel(const CacheAttnArgs a, int ctas, int w_blocks)
     x -= 16 * ctas;
     if (x < c.B) {
         const CacheSeq s = cache_seq(c, x);
-        if (s.bits && threadIdx.x == 0)
-            atomicOr(&c.hdr->flag, s.bits);
+        if (threadIdx.x == 0) {
+            const int bits = s.bits | cache_offset_bits(c, x);
+            if (bits)
+                atomicOr(&c.hdr->flag, bits);
+        }
         if (s.bits || s.len > 0)
             return;
         const int64_t width = (int64_t)c.H * D;

@@ -164,6 +164,9 @@ cudaError_t launch_jagged_truncate(const int64_t *off, const int32_t *nt, int B,
                                    int64_t row_bytes, const void *in, void *out, int64_t *out_off,
                                    cudaStream_t stream);
 
+// 8-bit cache: an append or attention of no sequences checks its offsets all the same.
+cudaError_t launch_cache_no_sequences(const CacheCall &c, cudaStream_t stream);
+
 // 8-bit cache: append of new tokens (k, v rows ldk, ldv elements apart).
 int cache_append_blocks(int max_seq_len);
 cudaError_t launch_cache_append(const CacheCall &c, bool bf16, const void *k, int64_t ldk, const void *v, int64_t ldv,
