@@ -128,7 +128,8 @@ cache_attn_rows_kernel(const CacheAttnArgs a)
     int p = p0 + warp;
     int page = page_of(p);
     if (page >= 0) {
-        load(c.k_codes, kbuf, kbar, page);
+        if (!(a.withhold && blockIdx.x == 0 && warp == 0))
+            load(c.k_codes, kbuf, kbar, page);
         load(c.v_codes, vbuf, vbar, page);
     }
     if (threadIdx.x < R) {
@@ -225,7 +226,7 @@ cache_attn_rows_kernel(const CacheAttnArgs a)
             }
         }
         __syncwarp();
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(kbar, loads & 1, &abort_flag, c.hdr)))) {
+        if (!(ok = mbar_wait_warp(kbar, loads & 1, &abort_flag, c.hdr, a.wait_limit))) {
             mbar_drain(kbar, loads & 1);
             mbar_drain(vbar, loads & 1);
             break;
@@ -304,7 +305,7 @@ cache_attn_rows_kernel(const CacheAttnArgs a)
                     wplane[p * kPage + key0 + 2 * i] = wsum[i];
             }
         }
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(vbar, loads & 1, &abort_flag, c.hdr)))) {
+        if (!(ok = mbar_wait_warp(vbar, loads & 1, &abort_flag, c.hdr, a.wait_limit))) {
             mbar_drain(kbar, (loads + (next >= 0)) & 1);
             mbar_drain(vbar, loads & 1);
             break;

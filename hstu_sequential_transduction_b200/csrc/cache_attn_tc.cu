@@ -399,9 +399,7 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
         start.k = (int)found[1] % start.z.kt;
     }
     bool ok = true;
-    auto wait = [&](int i, int parity) { return mbar_wait(bar(i), parity & 1, abort_flag, hdr); };
-    // by a whole warp that stays converged
-    auto wait_all = [&](int i, int parity) { return __all_sync(0xffffffffu, wait(i, parity)) != 0; };
+    auto wait = [&](int i, int parity) { return mbar_wait_warp(bar(i), parity & 1, abort_flag, hdr, a.wait_limit); };
 
     if (warp == 0) {
         // ---------------- codes ----------------
@@ -425,10 +423,11 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
                 const int sc0 = __shfl_sync(0xffffffffu, held_scale, 2 * (t % 16));
                 const int sc1 = __shfl_sync(0xffffffffu, held_scale, 2 * (t % 16) + 1);
                 const uint32_t bytes = ((page[0] >= 0) + (page[1] >= 0)) * kPage * D;
-                ok = g < kKStages || wait_all(K_EMPTY + kst, g / kKStages - 1);
+                ok = g < kKStages || wait(K_EMPTY + kst, g / kKStages - 1);
                 if (!ok)
                     break;
-                if (elect_one()) {
+                // (the hook: of the last CTA, whose run has tiles if any has)
+                if (elect_one() && !(a.withhold && g == 0 && blockIdx.x == gridDim.x - 1)) {
                     mbar_expect_tx(bar(K_FULL + kst), bytes);
 #pragma unroll
                     for (int e = 0; e < 2; e++)
@@ -437,7 +436,7 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
                                         (page[e] * c.H + h) * kPage, bar(K_FULL + kst));
                 }
                 k_loads = g + 1;
-                ok = g < kVStages || wait_all(C_EMPTY + vst, g / kVStages - 1);
+                ok = g < kVStages || wait(C_EMPTY + vst, g / kVStages - 1);
                 if (!ok)
                     break;
                 if (elect_one()) {
@@ -462,7 +461,7 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
         int g = 0, it = 0;
         for (int piece = 0; ok; piece++) {
             const int qs = piece & 1;
-            if (!(ok = wait_all(Q_FULL + qs, piece >> 1)))
+            if (!(ok = wait(Q_FULL + qs, piece >> 1)))
                 break;
             const int count = info[qs].count, halves = info[qs].cols > 64 ? 2 : 1;
             if (count == 0)
@@ -470,14 +469,14 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
             for (int t = 0; ok && t < count; t++, g++) {
                 const int st = g % kKStages;
                 // the key data too: S_FULL then stands for both
-                if (!(ok = wait_all(K_FULL + st, g / kKStages) && wait_all(KEY_FULL + g % kKeySlots, g / kKeySlots)))
+                if (!(ok = wait(K_FULL + st, g / kKStages) && wait(KEY_FULL + g % kKeySlots, g / kKeySlots)))
                     break;
                 // both halves at once where their buffers are neighbours
                 const int wide = halves == 2 && (it & 1) == 0 ? 2 : 1;
                 for (int hf = 0; hf < halves; hf += wide, it += wide) {
                     // a buffer is free once the item four back has become P^T
-                    ok = (it < 4 || wait_all(P_FULL + (it & 3), (it >> 2) - 1)) &&
-                         (wide == 1 || it < 4 || wait_all(P_FULL + (it & 3) + 1, (it >> 2) - 1));
+                    ok = (it < 4 || wait(P_FULL + (it & 3), (it >> 2) - 1)) &&
+                         (wide == 1 || it < 4 || wait(P_FULL + (it & 3) + 1, (it >> 2) - 1));
                     if (!ok)
                         break;
                     tc_fence_after();
@@ -507,7 +506,7 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
         int g = 0, it = 0;
         for (int piece = 0; ok; piece++) {
             const int qs = piece & 1;
-            if (!(ok = wait_all(Q_FULL + qs, piece >> 1)))
+            if (!(ok = wait(Q_FULL + qs, piece >> 1)))
                 break;
             const int count = info[qs].count, halves = info[qs].cols > 64 ? 2 : 1;
             if (count == 0)
@@ -515,14 +514,14 @@ cache_attn_tc_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_const
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(bar(Q_EMPTY + qs));
-            if (piece > 0 && !(ok = wait_all(O_FREE, piece - 1)))
+            if (piece > 0 && !(ok = wait(O_FREE, piece - 1)))
                 break;
             for (int t = 0; ok && t < count; t++, g++) {
                 const int vb = g & 1;
-                if (!(ok = wait_all(V_FULL + vb, g >> 1)))
+                if (!(ok = wait(V_FULL + vb, g >> 1)))
                     break;
                 for (int hf = 0; hf < halves; hf++, it++) {
-                    if (!(ok = wait_all(P_FULL + (it & 3), it >> 2)))
+                    if (!(ok = wait(P_FULL + (it & 3), it >> 2)))
                         break;
                     tc_fence_after();
                     if (elect_one()) {

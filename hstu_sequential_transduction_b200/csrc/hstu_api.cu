@@ -274,13 +274,21 @@ CacheCall cache_call(const hstu_cache *c, int32_t B, int32_t max_cache_len, cons
 // rows `stride` elements apart of a [T, H, d] tensor: dense enough and 16-byte aligned
 bool row_stride_ok(int64_t stride, int64_t width, size_t elem) { return stride >= width && stride * elem % 16 == 0; }
 
+bool cache_wait_test(const hstu_attn_desc *d) { return d->debug_checks == HSTU_DEBUG_CACHE_WAIT_TEST; }
+
 hstu_status check_cache_attn(const hstu_attn_desc *d, const hstu_cache *c, int32_t max_cache_len)
 {
-    HSTU_TRY(check_attn_desc(d));
+    if (!d)
+        return HSTU_ERR_INVALID_ARG;
+    hstu_attn_desc plain = *d;
+    if (cache_wait_test(d))
+        plain.debug_checks = 0;
+    HSTU_TRY(check_attn_desc(&plain));
     HSTU_TRY(check_cache(c));
     if (max_cache_len < 0 || d->num_heads != c->num_heads || d->d_qk != c->head_dim)
         return HSTU_ERR_INVALID_ARG;
-    if (d->fp8_qk || d->debug_checks || d->local_window || d->global_window)
+    if (d->fp8_qk || plain.debug_checks || d->local_window || d->global_window ||
+        (cache_wait_test(d) && d->dtype != HSTU_BF16))  // the float32 kernel waits for nothing
         return HSTU_ERR_UNSUPPORTED;
     // a longer cache than the tables have room for is never read
     if (max_cache_len > c->max_pages * HSTU_CACHE_PAGE)
@@ -891,6 +899,8 @@ hstu_status hstu_cache_attn_fwd(const hstu_attn_desc *desc, const hstu_cache *ca
     a.addend = addend;
     a.out = out;
     a.weights_out = weights_out;
+    a.wait_limit = cache_wait_test(desc) ? kTestWaitLimitCycles : kWaitLimitCycles;
+    a.withhold = cache_wait_test(desc);
     char *cur = static_cast<char *>(workspace) + sizeof(WsHeader);
     a.part_o = reinterpret_cast<float *>(cur);
     a.part_w = weights_out ? reinterpret_cast<float *>(cur + a.plan.part_o_bytes) : nullptr;

@@ -214,6 +214,10 @@ struct CacheAttnArgs {
     float *weights_out;
     float *part_o, *part_w;
     CacheAttnPiece *pieces;
+    // cycles after which a wait of the bf16 kernels gives up, and its test hook: one
+    // CTA's first block of keys is never loaded
+    long long wait_limit;
+    int withhold;
 };
 CacheAttnPlan cache_attn_plan(const CacheCall &c, bool bf16, bool with_weights);
 bool cache_attn_fits(const CacheAttnArgs &a);  // its launches and coordinates stay below their limits

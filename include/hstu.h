@@ -76,6 +76,10 @@ typedef enum { HSTU_F32 = 0, HSTU_BF16 = 1 } hstu_dtype;
  * workspace clears the flag.  For tests of the timeout path only. */
 #define HSTU_DEBUG_WAIT_TEST 2
 
+/* The same hook of the two bf16 kernels of hstu_cache_attn_fwd; an invalid
+ * argument in any other call.  One CTA's first block of keys is never loaded. */
+#define HSTU_DEBUG_CACHE_WAIT_TEST 4
+
 typedef struct {
     int32_t num_seqs;         /* B >= 0 */
     int32_t max_seq_len;      /* >= every L_b; sizes the schedule */
@@ -87,7 +91,7 @@ typedef struct {
     float inv_n;              /* the 1/N scale applied after SiLU */
     int32_t pos_lo, pos_hi;   /* rab_pos covers distances pos_lo..pos_hi */
     int32_t num_time_buckets; /* NB >= 1 */
-    /* 0, or HSTU_DEBUG_WAIT_TEST (hstu_attn_fwd only; see below).  The device
+    /* 0, or a test hook above (HSTU_DEBUG_WAIT_TEST: hstu_attn_fwd only).  The device
      * input checks of seq_offsets and num_targets always run. */
     int32_t debug_checks;
     /* Semi-local attention (the ULTRA-HSTU review's local + global windows):
@@ -370,7 +374,8 @@ hstu_status hstu_cache_attn_workspace_size(const hstu_attn_desc *desc, const hst
  * too with cand_positions = 1).  Biases, clamps and tables as in hstu_attn_fwd.  A sequence with
  * an empty cache gets its addend, or zeros; the rows of a dropped one and rows
  * behind the last sequence are left as they were.
- *   desc       the call's tokens; fp8_qk, debug_checks and the windows must be 0
+ *   desc       the call's tokens; fp8_qk and the windows must be 0, debug_checks 0
+ *              or HSTU_DEBUG_CACHE_WAIT_TEST
  *   max_cache_len >= every cache_lens[b]; sizes the launch and the workspace
  *   q          [T, H, d], rows q_stride elements apart, 16-byte aligned
  *   addend     [T, H, d] of q's type or NULL; may be `out`

@@ -167,3 +167,17 @@ def test_a_cache_keeps_its_tensors():
     cache._structs = {}
     with pytest.raises(AttributeError, match="keeps its tensors"):
         cache.weights = None
+
+
+def test_wait_test_hook():
+    """Taken by the bf16 attention over the cache and by no other call."""
+    n = ctypes.c_size_t(0)
+    d = _desc()
+    d.debug_checks = ops.HSTU_DEBUG_CACHE_WAIT_TEST
+    assert _attn(desc=d, ws=0) == WORKSPACE  # past the descriptor's checks
+    f32 = _desc(dtype=ops.HSTU_F32)
+    f32.debug_checks = ops.HSTU_DEBUG_CACHE_WAIT_TEST
+    assert _attn(desc=f32) == UNSUPPORTED
+    assert ops.load_library().hstu_attn_workspace_size(ctypes.byref(d), 0, ctypes.byref(n)) == INVALID
+    d.debug_checks = 8
+    assert _attn(desc=d) == INVALID

@@ -70,3 +70,51 @@ def test_append_of_no_sequences(off, T, bits, cuda_device):
                           torch.zeros(T, dtype=torch.int64, device=cuda_device), None, max_seq_len=4, workspace=ws)
     assert ops.hstu_check_device_flag(ws) == (5 if bits else 0, bits)
     assert_pool_equal(pool_of(cache), pool)
+
+
+# ---- a wait that runs out -------------------------------------------------------------
+
+WAITS = [(64, 1), (64, 30), (128, 8), (128, 64), (64, 65), (128, 200)]
+
+
+def _withheld(monkeypatch):
+    """From here on one CTA of an attention never gets its first keys."""
+    def desc(*args, real=ops._cache_attn_desc):
+        d = real(*args)
+        d.debug_checks = ops.HSTU_DEBUG_CACHE_WAIT_TEST
+        return d
+
+    monkeypatch.setattr(ops, "_cache_attn_desc", desc)
+
+
+def _wait_inputs(d, n, device):
+    rng = np.random.default_rng(n)
+    lens = [1100, 300, 700]
+    pool, table, _, _ = make_pool(rng, lens, 2, d)
+    cache = to_cache(pool, device)
+    q = torch.as_tensor(rng.standard_normal((3 * n, 2, d)), dtype=torch.float32).to(torch.bfloat16).to(device)
+    args = dict(max_seq_len=n, max_cache_len=max(lens), inv_n=1 / 64, pos_lo=-32, pos_hi=32)
+    rp, rt = (0.1 * torch.randn(m, generator=torch.Generator().manual_seed(m)).to(device) for m in (65, 16))
+    t = dev(table, device, torch.int32)
+    inputs = (q, cache, t, dev(lens, device, torch.int32), None, dev(n * np.arange(4), device, torch.int64),
+              1_700_000_000 + torch.arange(3 * n, device=device), None, rp, rt)
+    size = ops.hstu_cache_attn_workspace_size(q, cache, t, rp, rt, weights=True, **args)
+    return cache, inputs, args, size
+
+
+@pytest.mark.parametrize("d,n", WAITS)
+def test_bounded_waits_of_the_attention_run_out(d, n, cuda_device, monkeypatch):
+    """The kernel ends and reports, and the next call on the same workspace is as any other."""
+    cache, inputs, args, size = _wait_inputs(d, n, cuda_device)
+    ws = ops.alloc_workspace(size, cuda_device)
+    want_w = torch.zeros_like(cache.weights)
+    want = ops.hstu_cache_attn_fwd(*inputs, weights_out=want_w, workspace=ws, **args)
+    assert ops.hstu_check_device_flag(ws) == (0, 0)
+    with monkeypatch.context() as m:
+        _withheld(m)
+        ops.hstu_cache_attn_fwd(*inputs, weights_out=torch.zeros_like(want_w), workspace=ws, **args)
+        assert ops.hstu_check_device_flag(ws) == (5, 32)
+    wout = torch.zeros_like(want_w)
+    out = ops.hstu_cache_attn_fwd(*inputs, weights_out=wout, workspace=ws, **args)
+    assert ops.hstu_check_device_flag(ws) == (0, 0)
+    assert torch.equal(out, want) and torch.equal(wout, want_w)
