@@ -69,10 +69,13 @@ __device__ __forceinline__ int table_page(const int32_t *table, const CacheCall 
 }
 
 // weights_out of cached tokens j .. j + 3 of sequence b (j a multiple of 4): what they
-// had plus their planes, in order.
+// had plus their planes, in order.  After a wait that ran out planes are missing: nothing is
+// written, for weights that go on from call to call would never lose the damage.
 __device__ __forceinline__ void cache_join_weights(const CacheAttnArgs &a, int b, int j)
 {
     const CacheCall &c = a.c;
+    // the kernel before has ended; read here and looked at last, it costs no time of its own
+    const bool whole = !(__ldcg(&c.hdr->flag) & FLAG_TIMEOUT);
     const CacheSeq s = cache_seq(c, b);
     if (j >= s.len)
         return;
@@ -91,7 +94,7 @@ __device__ __forceinline__ void cache_join_weights(const CacheAttnArgs &a, int b
     const float add[4] = {sum.x, sum.y, sum.z, sum.w}, scale = fabsf(a.inv_n);
 #pragma unroll
     for (int e = 0; e < 4; e++)
-        if (j + e < s.len)
+        if (whole && j + e < s.len)
             a.weights_out[at + e] = fmaf(scale, add[e], c.weights ? c.weights[at + e] : 0.f);
 }
 

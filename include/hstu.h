@@ -383,6 +383,8 @@ hstu_status hstu_cache_attn_workspace_size(const hstu_attn_desc *desc, const hst
  *              starts from 0 where that is NULL.  Only the cached tokens of the
  *              call's sequences are written; with weights_out these sequences
  *              must not share pages.
+ * After a pipeline wait that ran out (bit 32 of the flag) `out` is undefined, and
+ * weights_out is left as it was.
  * float32 q is computed to float32 accuracy.  For bf16 q sums are float32, and
  *   max_seq_len <= 64: an element of q is held to 2^-39 of its row's largest, P is
  *     rounded to 11 bits;

@@ -118,3 +118,18 @@ def test_bounded_waits_of_the_attention_run_out(d, n, cuda_device, monkeypatch):
     out = ops.hstu_cache_attn_fwd(*inputs, weights_out=wout, workspace=ws, **args)
     assert ops.hstu_check_device_flag(ws) == (0, 0)
     assert torch.equal(out, want) and torch.equal(wout, want_w)
+
+
+@pytest.mark.parametrize("d,n", WAITS)
+@pytest.mark.parametrize("same", [False, True])
+def test_weights_survive_a_wait_that_runs_out(d, n, same, cuda_device, monkeypatch):
+    """A flagged call adds nothing to the weights that later evictions go by."""
+    cache, inputs, args, size = _wait_inputs(d, n, cuda_device)
+    ws = ops.alloc_workspace(size, cuda_device)
+    ws.fill_(255)  # NaN where nothing is written
+    wout = cache.weights if same else torch.full_like(cache.weights, -5.0)
+    before = wout.clone()
+    _withheld(monkeypatch)
+    ops.hstu_cache_attn_fwd(*inputs, weights_out=wout, workspace=ws, **args)
+    assert ops.hstu_check_device_flag(ws) == (5, 32)
+    assert torch.equal(wout, before)
