@@ -226,7 +226,7 @@ cache_attn_rows_kernel(const CacheAttnArgs a)
             }
         }
         __syncwarp();
-        if (!(ok = mbar_wait_warp(kbar, loads & 1, &abort_flag, c.hdr, a.wait_limit))) {
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(kbar, loads & 1, &abort_flag, c.hdr, a.wait_limit)))) {
             mbar_drain(kbar, loads & 1);
             mbar_drain(vbar, loads & 1);
             break;
@@ -305,7 +305,7 @@ cache_attn_rows_kernel(const CacheAttnArgs a)
                     wplane[p * kPage + key0 + 2 * i] = wsum[i];
             }
         }
-        if (!(ok = mbar_wait_warp(vbar, loads & 1, &abort_flag, c.hdr, a.wait_limit))) {
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(vbar, loads & 1, &abort_flag, c.hdr, a.wait_limit)))) {
             mbar_drain(kbar, (loads + (next >= 0)) & 1);
             mbar_drain(vbar, loads & 1);
             break;
