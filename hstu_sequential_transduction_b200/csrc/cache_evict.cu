@@ -271,16 +271,16 @@ __device__ __forceinline__ __half2 codes_half2(uint32_t codes)
     return *reinterpret_cast<const __half2 *>(&h);
 }
 
-// the larger of m and four codes' magnitudes, two and two
+// the larger of m and four codes' magnitudes, two and two; NaN wins
 __device__ __forceinline__ __half2 max_codes(__half2 m, uint32_t w)
 {
-    return __hmax2(m, __hmax2(__habs2(codes_half2(w)), __habs2(codes_half2(w >> 16))));
+    return __hmax2_nan(m, __hmax2_nan(__habs2(codes_half2(w)), __habs2(codes_half2(w >> 16))));
 }
 
 // bits of the larger of a pair of magnitudes, times the scale
 __device__ __forceinline__ uint32_t magnitude(__half2 m, float scale)
 {
-    return __float_as_uint(fmaxf(__low2float(m), __high2float(m)) * scale) & 0x7fffffffu;
+    return __float_as_uint(__half2float(__hmax_nan(__low2half(m), __high2half(m))) * scale) & 0x7fffffffu;
 }
 
 // four codes re-rounded, each with its own ratio: one rounding, the products are exact
