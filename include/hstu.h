@@ -317,7 +317,10 @@ hstu_status hstu_gemm_e4m3(const void *codes, const float *scales, int64_t M, in
  * so a code is the value's one rounding to E4M3 (nearest even), and a block
  * whose scale grows shifts its older codes (rounding again only those that
  * leave E4M3's normal range).  A pool that was filled in another way needs scales
- * that are powers of two, 0 or NaN, too.
+ * that are powers of two, 0 or NaN, too, and no code 0x7f or 0xff (NaN) among its
+ * cached tokens but under a NaN scale: the attention reads such a value's code as
+ * NaN or as +-480, depending on max_seq_len.  A value that is not finite is stored
+ * as its block's NaN scale, as the append does.
  *
  * Device checks add two bits to those of hstu_check_device_flag:
  * 64 = cache_lens outside [0, max_cache_len] or the table's room, or tokens
