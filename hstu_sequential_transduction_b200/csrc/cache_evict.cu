@@ -522,7 +522,7 @@ cudaError_t launch_cache_evict(const CacheCall &c, int keep, int first, int rece
     else
         cache_select_kernel<1024><<<c.B, 1024, 0, stream>>>(c, keep, first, recent, new_pages, new_table, new_lens,
                                                             kept, keys, cap);
-    if (c.max_cache_len > keep) {
+    if (c.max_cache_len > keep && c.max_pages > 0) {
         const int blocks = std::min((keep + kPage - 1) / kPage, c.max_pages);
         switch (c.d) {
         case 32: move<32>(c, keep, blocks, new_pages, kept, stream); break;
