@@ -27,8 +27,13 @@ def test_evict_with_tables_of_no_pages(cuda_device):
 
 # ---- calls at the same time -----------------------------------------------------------
 
-def _attention(dtype, d, n, lens, device, seed):
-    """A prepared attention: a call that repeats it, and what it writes."""
+def _workspace(ws, size, device):
+    assert ws is None or ws.numel() >= size
+    return ops.alloc_workspace(size, device) if ws is None else ws
+
+
+def _attention(dtype, d, n, lens, device, seed, ws=None):
+    """A prepared attention: a call that repeats it, what it writes, and its workspace."""
     rng = np.random.default_rng(seed)
     pool, table, _, _ = make_pool(rng, lens, 2, d)
     cache = to_cache(pool, device)
@@ -41,11 +46,11 @@ def _attention(dtype, d, n, lens, device, seed):
     inputs = (q, cache, t, dev(lens, device, torch.int32), None, dev(n * np.arange(len(lens) + 1), device, torch.int64),
               1_700_000_000 + 50 * torch.arange(T, device=device), None, rp, rt)
     out, wout = torch.empty_like(q), torch.zeros_like(cache.weights)
-    ws = ops.alloc_workspace(ops.hstu_cache_attn_workspace_size(q, cache, t, rp, rt, weights=True, **args), device)
+    ws = _workspace(ws, ops.hstu_cache_attn_workspace_size(q, cache, t, rp, rt, weights=True, **args), device)
     return lambda: ops.hstu_cache_attn_fwd(*inputs, out=out, weights_out=wout, workspace=ws, **args), (out, wout), ws
 
 
-def _append(n, lens, device, seed):
+def _append(n, lens, device, seed, ws=None):
     """The same tokens appended again and again behind the same lengths: the same bytes."""
     rng = np.random.default_rng(seed)
     pool, table, _, _ = make_pool(rng, [x + n for x in lens], 2, 64)
@@ -55,12 +60,12 @@ def _append(n, lens, device, seed):
     inputs = (k, v, cache, dev(table, device, torch.int32), dev(lens, device, torch.int32), None,
               dev(n * np.arange(len(lens) + 1), device, torch.int64), torch.arange(T, device=device), None)
     new = [torch.zeros(len(lens), dtype=torch.int32, device=device) for _ in range(2)]
-    ws = ops.alloc_workspace(ops.hstu_cache_append_workspace_size(), device)
+    ws = _workspace(ws, ops.hstu_cache_append_workspace_size(), device)
     call = lambda: ops.hstu_cache_append(*inputs, max_seq_len=n, new_lens=new[0], new_pos=new[1], workspace=ws)  # noqa: E731
     return call, (cache.k_codes, cache.v_codes, cache.k_scale, cache.v_scale, *new), ws
 
 
-def _evict(lens, keep, device, seed):
+def _evict(lens, keep, device, seed, ws=None):
     rng = np.random.default_rng(seed)
     cols = -(-max(lens) // 64)
     pool, table, free, _ = make_pool(rng, lens, 2, 64, extra=len(lens) * -(-keep // 64), cols=cols)
@@ -69,7 +74,7 @@ def _evict(lens, keep, device, seed):
     new_pages[:, :-(-keep // 64)] = free.reshape(len(lens), -1)
     t, n = dev(table, device, torch.int32), dev(new_pages, device, torch.int32)
     kw = dict(keep=keep, first=4, recent=32, max_cache_len=max(lens))
-    ws = ops.alloc_workspace(ops.hstu_cache_evict_workspace_size(cache, t, **kw), device)
+    ws = _workspace(ws, ops.hstu_cache_evict_workspace_size(cache, t, **kw), device)
     new = (torch.zeros_like(t), torch.zeros(len(lens), dtype=torch.int32, device=device),
            torch.zeros(len(lens), keep, dtype=torch.int32, device=device))
     ln = dev(lens, device, torch.int32)
@@ -78,12 +83,12 @@ def _evict(lens, keep, device, seed):
     return call, (cache.k_codes, cache.v_codes, cache.k_scale, cache.v_scale, *new), ws
 
 
-MAKE = {"cores": lambda dv, s: _attention("bf16", 128, 200, [4000, 900], dv, s),
-        "cores64": lambda dv, s: _attention("bf16", 64, 70, [1500, 3000, 64], dv, s),
-        "rows": lambda dv, s: _attention("bf16", 128, 9, [6000, 100, 2000], dv, s),
-        "f32": lambda dv, s: _attention("f32", 32, 12, [900, 500], dv, s),
-        "append": lambda dv, s: _append(300, [70, 0, 129], dv, s),
-        "evict": lambda dv, s: _evict([6000, 5000], 1000, dv, s)}
+MAKE = {"cores": lambda *a: _attention("bf16", 128, 200, [4000, 900], *a),
+        "cores64": lambda *a: _attention("bf16", 64, 70, [1500, 3000, 64], *a),
+        "rows": lambda *a: _attention("bf16", 128, 9, [6000, 100, 2000], *a),
+        "f32": lambda *a: _attention("f32", 32, 12, [900, 500], *a),
+        "append": lambda *a: _append(300, [70, 0, 129], *a),
+        "evict": lambda *a: _evict([6000, 5000], 1000, *a)}
 
 
 @pytest.mark.parametrize("one,two", [("cores", "cores"), ("cores64", "rows"), ("cores", "append"), ("rows", "rows"),
@@ -119,3 +124,28 @@ def test_calls_in_flight_together(one, two, cuda_device):
         assert ops.hstu_check_device_flag(ws) == (0, 0)
         for a, b in zip(outs, w):
             assert torch.equal(a, b)
+
+
+def test_captured_calls_share_a_workspace(cuda_device):
+    """A graph of each kind of call, all on one workspace, replayed in turn and again."""
+    kinds = list(MAKE)
+    want = []
+    for kind in kinds:
+        call, outs, _ = MAKE[kind](cuda_device, 7)
+        call()
+        want.append([t.clone() for t in outs])
+    ws = ops.alloc_workspace(1 << 26, cuda_device)
+    ws.fill_(255)
+    calls = [MAKE[kind](cuda_device, 7, ws) for kind in kinds]
+    graphs = []
+    torch.cuda.synchronize()
+    for call, _, _ in calls:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            call()
+    for order in (range(len(kinds)), reversed(range(len(kinds)))):
+        for i in order:
+            graphs[i].replay()
+            assert ops.hstu_check_device_flag(ws) == (0, 0)
+            for a, b in zip(calls[i][1], want[i]):
+                assert torch.equal(a, b), kinds[i]
