@@ -8,7 +8,7 @@
 // Bound by HBM: each k and v element is read once and its code written once (98,000
 // tokens of 4 heads, d = 128: 64 us, 4.8 TB/s, with four CTAs an SM, for bf16; 68 with
 // three, which float32's registers allow; 86 with two, 127 with the rows widened to
-// floats before the reduction).  Issue slots are next, 2/3 busy.
+// floats before the reduction).  Issue slots are next, 70 % busy.
 // One CTA per (sequence, block, head), 2 D threads: a thread takes 4 tokens x 8
 // dims of K and of V, all eight 16-byte (bf16) loads in flight before the one
 // reduction.  Keys leave as 8 bytes per token (16 lanes fill a 128-byte row).

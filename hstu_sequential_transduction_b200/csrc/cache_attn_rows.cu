@@ -196,7 +196,7 @@ cache_attn_rows_kernel(const CacheAttnArgs a)
             continue;
         }
         const float ks = c.k_scale[(int64_t)page * c.H + h], vs = c.v_scale[(int64_t)page * c.H + h];
-        // biases of keys lane and lane + 32 for every row, the table reads of four rows in flight
+        // biases of keys lane and lane + 32 for every row, the table reads of eight rows in flight
         __syncwarp();
         int pj[2];
         int64_t tj[2];

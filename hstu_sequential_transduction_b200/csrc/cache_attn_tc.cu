@@ -22,13 +22,17 @@
 //
 // Per 128 x 128 tile at d = 128 the tensor pipe, MUFU (one tanh per pair) and shared
 // memory need 1024 cycles each; V^T as a TMEM operand is what keeps the last there.  The
-// kernel takes ~2,200: it is bound by its issue slots (~8,000 warp instructions a tile,
-// half of them the math).  So what a tile needs besides is spread over many warps:
+// kernel takes ~2,700 (10,784 tiles of 109 columns on average, 256-512 candidates over
+// 8k-16k tokens: 196,000 cycles an SM): it is bound by its issue slots, 68 % busy with
+// ~7,300 warp instructions a tile, half of them the math, and by the code that seven roles
+// fetch (waits whose loops were inlined cost a fifth).  72 registers a thread are all that
+// 896 threads leave, and some spill (268 bytes of stores at d = 128, 144 at d = 64).  So what
+// a tile needs besides is spread over many warps:
 // Warp roles (896 threads): 0 loads the codes (TMA); 1 issues S^T and owns TMEM; 2 issues
 // O^T (3 idle); 4-19, four groups, take 64 columns of a tile in turn from S^T to P^T,
 // each with a buffer of S^T and one of P^T; 20-27, two groups, take every other tile's
 // keys (bias, scale) and values (conversion), and together split the queries.
-// (16 users x 512 candidates over 2048 tokens, 2 heads: 38 us; one conversion group 43,
+// (16 users x 512 candidates over 2048 tokens, 2 heads: 37 us; one conversion group 43,
 // the keys' data fetched by the epilogue warps 45, two epilogue groups of 128 columns 48.)
 // TMEM columns: S^T 4 x 64, O^T [256, 384), V^T [384, 448), [448, 512).
 //
@@ -51,7 +55,11 @@ namespace {
 constexpr int kTile = 128;    // keys of a tile, query columns of a unit
 constexpr int kThreads = 896;
 constexpr int kKStages = 3, kVStages = 2;  // tiles of codes in flight
-constexpr int kCutTiles = 8;  // what a cut unit costs (its pieces' traffic and the join), in tiles
+// What a cut unit costs (its pieces' traffic and the join), in tiles: units of one length stay
+// whole where that makes no run longer by more.  Without it 16 x 512 candidates over 2048 tokens
+// of 2 heads take 43.5 us for 37.0, and 30 x 512 over 1024 take 55 for 43 (but 40 x 128 over 512
+// of 4 heads 32.6 for 34.2); with no limit 20 x 512 over 2048 take 62 for 47.
+constexpr int kCutTiles = 8;
 constexpr int kPanel = 16384; // 64 query columns of P^T: 128 keys x 128 bytes
 
 constexpr int kKeySlots = 4;  // tiles of key data ahead

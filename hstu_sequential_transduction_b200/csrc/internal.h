@@ -185,6 +185,10 @@ cudaError_t launch_cache_evict(const CacheCall &c, int keep, int first, int rece
 // with two slots [128, d] of part_o and two piece records each.  Where weights are
 // taken, those of plane_rows queries and one head go to a plane of part_w [planes, B, lcap].  A second
 // kernel joins them in a fixed order.
+// At 64 rows both sides win somewhere (d = 128, 4 heads, few rows' kernel / tensor cores): one
+// user's 2,048 cached tokens 14 / 23-31 us (candidates - history), 16,384 tokens 47 / 37-48;
+// 32 users' 1,024 tokens 71 / 25-46, 8,192 tokens 332 / 83-180.  At 8 rows the first one wins
+// (11 / 23, 18 / 35-38, 19 / 23-29) but for the longest batch's candidates (81 / 78-99).
 constexpr int kCacheRows = 64;
 enum CacheKernel { CACHE_F32, CACHE_ROWS, CACHE_TC };
 struct CacheAttnPlan {

@@ -349,7 +349,9 @@ hstu_status hstu_cache_append_workspace_size(size_t *bytes);
  * are candidates) to the cache.  k, v: [total_tokens, H, d] of `dtype`, rows
  * k_stride and v_stride elements apart (multiples of 16 bytes; H * d where
  * dense), 16-byte aligned; d is 64 or 128 for HSTU_BF16, 32 or 64 for HSTU_F32.
- * Token i of the call gets position seq_pos[b] + i and weight 0.  new_lens
+ * Token i of the call gets position seq_pos[b] + i and weight 0: tokens of one call
+ * give each other none, so until an attention with weights_out has run over them, an
+ * eviction keeps the lowest indices among them.  new_lens
  * (cache_lens + appended) and new_pos (seq_pos + appended, may be NULL) are
  * int32 [B] and must not overlap cache_lens and seq_pos.  A dropped sequence
  * keeps its length.  The pages a call writes must belong to one sequence each;
@@ -385,10 +387,12 @@ hstu_status hstu_cache_attn_workspace_size(const hstu_attn_desc *desc, const hst
  *   weights_out float32 [num_pages, 64] or NULL; may be cache->weights, and
  *              starts from 0 where that is NULL.  Only the cached tokens of the
  *              call's sequences are written; with weights_out these sequences
- *              must not share pages.
+ *              must not share pages, nor a page occur twice.
  * After a pipeline wait that ran out (bit 32 of the flag) `out` is undefined, and
  * weights_out is left as it was.
- * float32 q is computed to float32 accuracy.  For bf16 q sums are float32, and
+ * float32 q is computed to float32 accuracy.  For bf16 q sums are float32; SiLU takes
+ * the hardware's tanh, SiLU(s) = s / 2 (1 + tanh(s / 2)) to 2^-11 of the tanh, so that a
+ * pair is off by up to 2^-12 |s inv_n|, in weights_out too; and
  *   max_seq_len <= 64: an element of q is held to 2^-39 of its row's largest, P is
  *     rounded to 11 bits;
  *   above: q is held to 2^-14 of its row's largest at worst (two E4M3 parts under
